@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "moda_internal.h"
+#include "moda_paged.h"
 #include "symbol_addr.h"
 
 namespace moda {
@@ -522,6 +523,139 @@ moda_status moda_fwd_host(const void* q, const void* k, const void* v, const voi
     if (!fin || cudaEventRecord(fin, hp.so) != cudaSuccess || cudaStreamWaitEvent(s, fin, 0) != cudaSuccess)
         return fail(MODA_ERR_CUDA);
     return MODA_OK;
+}
+
+// ------------------------------------------------- paged sequence cache
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+moda_status fill_cache(PagedCache& c, const int32_t* cu_q, const int32_t* ctx_lens, const int32_t* block_table,
+                       int N, int B, int Hq, int Hkv, int d, int num_pages, int page_size, int max_blocks,
+                       moda_dtype dtype) {
+    if (N < 1 || B < 1 || Hq < 1 || Hkv < 1 || d < 1 || num_pages < 1 || page_size < 1 || max_blocks < 1)
+        return MODA_ERR_INVALID_VALUE;
+    if (Hq % Hkv) return MODA_ERR_INVALID_VALUE;
+    if (dtype != MODA_BF16 && dtype != MODA_F32) return MODA_ERR_INVALID_VALUE;
+    if (!cu_q || !ctx_lens || !block_table) return MODA_ERR_INVALID_VALUE;
+    if (!aligned4(cu_q) || !aligned4(ctx_lens) || !aligned4(block_table)) return MODA_ERR_MISALIGNED;
+    if (d > 128 || (d * (dtype == MODA_F32 ? 4 : 2)) % 16) return MODA_ERR_UNSUPPORTED;
+    if ((long long)page_size * d > 0x7fffffffLL) return MODA_ERR_UNSUPPORTED;  // rows of a page in 32 bits
+    c.cu_q = cu_q; c.ctx_lens = ctx_lens; c.block_table = block_table;
+    c.N = N; c.B = B; c.Hkv = Hkv; c.d = d;
+    c.num_pages = num_pages; c.page_size = page_size; c.max_blocks = max_blocks;
+    return MODA_OK;
+}
+
+moda_status run_append(const void* q, const void* k, const void* v, long long sq, long long sk, long long sv,
+                       const float* rope, int rope_len, int rot_dim, int interleaved, const int32_t* cu_q,
+                       const int32_t* ctx_lens, const int32_t* block_table, int N, int B, int Hq, int Hkv, int d,
+                       int num_pages, int page_size, int max_blocks, moda_dtype dtype, void* k_pages, void* v_pages,
+                       float* k_scale, float* v_scale, void* q_out, void* kd, void* vd, int Ld, int slot,
+                       void* stream) {
+    AppendArgs a;
+    std::memset(&a, 0, sizeof(a));
+    moda_status st = fill_cache(a.c, cu_q, ctx_lens, block_table, N, B, Hq, Hkv, d, num_pages, page_size, max_blocks,
+                                dtype);
+    if (st != MODA_OK) return st;
+    if (!k || !v || !k_pages || !v_pages || (!q) != (!q_out) || (!kd) != (!vd)) return MODA_ERR_INVALID_VALUE;
+    if (kd && (slot < 0 || slot >= Ld)) return MODA_ERR_INVALID_VALUE;
+    if (rope && (rope_len < 1 || rot_dim < 2 || rot_dim > d || rot_dim % 2)) return MODA_ERR_INVALID_VALUE;
+    if ((q && sq < (long long)Hq * d) || sk < (long long)Hkv * d || sv < (long long)Hkv * d)
+        return MODA_ERR_INVALID_VALUE;
+    const int per16 = dtype == MODA_F32 ? 4 : 8;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) ||
+        !aligned16(q_out) || !aligned16(kd) || !aligned16(vd) || !aligned4(rope) || !aligned4(k_scale) ||
+        !aligned4(v_scale) || (q && sq % per16) || sk % per16 || sv % per16)
+        return MODA_ERR_MISALIGNED;
+    a.q = q; a.k = k; a.v = v; a.sq = sq; a.sk = sk; a.sv = sv;
+    a.rope = rope; a.rope_len = rope_len; a.rot = rot_dim; a.interleaved = interleaved != 0;
+    a.Hq = Hq; a.dtype = dtype;
+    a.q_out = q_out; a.k_pages = k_pages; a.v_pages = v_pages; a.k_scale = k_scale; a.v_scale = v_scale;
+    a.kd = kd; a.vd = vd; a.Ld = Ld; a.slot = slot;
+    return launch_paged_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MODA_OK : MODA_ERR_LAUNCH;
+}
+
+moda_status run_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                          const float* v_scale, const void* kd, const void* vd, const int32_t* cu_q,
+                          const int32_t* ctx_lens, const int32_t* block_table, int N, int B, int max_q, int Hq,
+                          int Hkv, int d, int Ld, int Ld_cap, int num_pages, int page_size, int max_blocks,
+                          moda_dtype dtype, float scale, void* out, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream, moda_impl impl) {
+    if (impl != MODA_IMPL_AUTO && impl != MODA_IMPL_SIMT && impl != MODA_IMPL_TC && impl != MODA_IMPL_TC2)
+        return MODA_ERR_INVALID_VALUE;
+    PagedFwdArgs a;
+    std::memset(&a, 0, sizeof(a));
+    moda_status st = fill_cache(a.c, cu_q, ctx_lens, block_table, N, B, Hq, Hkv, d, num_pages, page_size, max_blocks,
+                                dtype);
+    if (st != MODA_OK) return st;
+    if (!q || !k_pages || !v_pages || !out || max_q < 1 || Ld < 0 || Ld > Ld_cap) return MODA_ERR_INVALID_VALUE;
+    if (Ld > 0 && (!kd || !vd)) return MODA_ERR_INVALID_VALUE;
+    if (!(scale == scale)) return MODA_ERR_INVALID_VALUE;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned4(lse) ||
+        !aligned4(k_scale) || !aligned4(v_scale) || (Ld > 0 && (!aligned16(kd) || !aligned16(vd))))
+        return MODA_ERR_MISALIGNED;
+    const size_t need = moda_fwd_paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, dtype);
+    if (need && (!workspace || workspace_bytes < need)) return MODA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MODA_ERR_MISALIGNED;
+    a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.k_scale = k_scale; a.v_scale = v_scale;
+    a.kd = kd; a.vd = vd; a.Hq = Hq; a.G = Hq / Hkv; a.Ld = Ld; a.Ld_cap = Ld_cap; a.max_q = max_q;
+    a.scale = scale; a.dtype = dtype; a.out = out; a.lse = lse; a.workspace = workspace;
+    if (impl == MODA_IMPL_TC || impl == MODA_IMPL_TC2) return MODA_ERR_UNSUPPORTED;
+    if (status_ptr(&a.status, &a.wait_limit) != cudaSuccess) return MODA_ERR_CUDA;
+    return launch_paged_fwd_simt(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MODA_OK : MODA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+moda_status moda_paged_append(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                              long long v_stride, const float* rope, int rope_len, int rot_dim, int interleaved,
+                              const int32_t* cu_q, const int32_t* ctx_lens, const int32_t* block_table, int N, int B,
+                              int Hq, int Hkv, int d, int num_pages, int page_size, int max_blocks, moda_dtype dtype,
+                              void* k_pages, void* v_pages, void* q_out, void* kd, void* vd, int Ld, int slot,
+                              void* stream) {
+    return run_append(q, k, v, q_stride, k_stride, v_stride, rope, rope_len, rot_dim, interleaved, cu_q, ctx_lens,
+                      block_table, N, B, Hq, Hkv, d, num_pages, page_size, max_blocks, dtype, k_pages, v_pages,
+                      nullptr, nullptr, q_out, kd, vd, Ld, slot, stream);
+}
+
+moda_status moda_paged_append_q8(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                                 long long v_stride, const float* rope, int rope_len, int rot_dim, int interleaved,
+                                 const int32_t* cu_q, const int32_t* ctx_lens, const int32_t* block_table, int N,
+                                 int B, int Hq, int Hkv, int d, int num_pages, int page_size, int max_blocks,
+                                 moda_dtype dtype, int8_t* k_pages, int8_t* v_pages, float* k_scale, float* v_scale,
+                                 void* q_out, void* kd, void* vd, int Ld, int slot, void* stream) {
+    if (!k_scale || !v_scale) return MODA_ERR_INVALID_VALUE;
+    return run_append(q, k, v, q_stride, k_stride, v_stride, rope, rope_len, rot_dim, interleaved, cu_q, ctx_lens,
+                      block_table, N, B, Hq, Hkv, d, num_pages, page_size, max_blocks, dtype, k_pages, v_pages,
+                      k_scale, v_scale, q_out, kd, vd, Ld, slot, stream);
+}
+
+size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d, moda_dtype dtype) {
+    (void)N; (void)B; (void)max_q; (void)Hq; (void)Hkv; (void)d; (void)dtype;
+    return 0;
+}
+
+moda_status moda_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* kd, const void* vd,
+                           const int32_t* cu_q, const int32_t* ctx_lens, const int32_t* block_table, int N, int B,
+                           int max_q, int Hq, int Hkv, int d, int Ld, int Ld_cap, int num_pages, int page_size,
+                           int max_blocks, moda_dtype dtype, float scale, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream, moda_impl impl) {
+    return run_fwd_paged(q, k_pages, v_pages, nullptr, nullptr, kd, vd, cu_q, ctx_lens, block_table, N, B, max_q, Hq,
+                         Hkv, d, Ld, Ld_cap, num_pages, page_size, max_blocks, dtype, scale, out, lse, workspace,
+                         workspace_bytes, stream, impl);
+}
+
+moda_status moda_fwd_paged_q8(const void* q, const int8_t* k_pages, const int8_t* v_pages, const float* k_scale,
+                              const float* v_scale, const void* kd, const void* vd, const int32_t* cu_q,
+                              const int32_t* ctx_lens, const int32_t* block_table, int N, int B, int max_q, int Hq,
+                              int Hkv, int d, int Ld, int Ld_cap, int num_pages, int page_size, int max_blocks,
+                              moda_dtype dtype, float scale, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream, moda_impl impl) {
+    if (!k_scale || !v_scale) return MODA_ERR_INVALID_VALUE;
+    return run_fwd_paged(q, k_pages, v_pages, k_scale, v_scale, kd, vd, cu_q, ctx_lens, block_table, N, B, max_q, Hq,
+                         Hkv, d, Ld, Ld_cap, num_pages, page_size, max_blocks, dtype, scale, out, lse, workspace,
+                         workspace_bytes, stream, impl);
 }
 
 moda_status moda_device_status(void* stream) {

@@ -337,6 +337,133 @@ moda_status moda_fwd_q8(const void* q, const void* k, const void* v,
 moda_status moda_depth_slot_layout(int B, int T, int Hkv, int d, int Ld, int slot,
                                    long long* offset, long long strides[4]);
 
+/*
+ * The paged sequence cache: serving a MoDA layer token by token. The read step
+ * ("Mixture-of-Depths Attention", gist.science German summary §2, Read-Step)
+ * needs the sequence keys of every earlier token but only the token's own
+ * depth keys, so the sequence keys and values live in pages that outlast a
+ * step, while the depth rows kd / vd belong to the step's new tokens. The
+ * pages describe the method, not its serving; the cache's layout is this
+ * library's.
+ *
+ * Layout and terms, shared by moda_paged_append*, moda_fwd_paged*:
+ *   - New tokens of B sequences are packed along one axis of N rows: sequence
+ *     b's are rows cu_q[b] .. cu_q[b+1]-1 (cu_q: int32 [B+1], non-decreasing;
+ *     a sequence may have none; rows outside every sequence are left alone).
+ *   - ctx_lens: int32 [B], tokens of each sequence WITH the new ones: row i of
+ *     sequence b sits at position ctx_lens[b] - (cu_q[b+1] - i).
+ *   - k_pages, v_pages [num_pages, Hkv, page_size, d]: block_table (int32
+ *     [B, max_blocks]) names the page of each page_size positions. Entries
+ *     outside [0, num_pages) mean "no page": such positions are not written
+ *     and not attended to; so are positions the table does not reach.
+ *   - 8-bit pages: int8 codes of that shape and one fp32 scale per (page,
+ *     kv-head) and tensor, k_scale, v_scale [num_pages, Hkv], always 0 or a
+ *     power of two: key = scale * code, exact in fp32 and in bf16.
+ *   - cu_q, ctx_lens and block_table are DEVICE arrays (4-byte aligned), read
+ *     by the kernels only, so a captured graph serves whatever they hold at
+ *     replay. Their values are not validated on the host; no value makes a
+ *     kernel read or write outside the buffers.
+ *   - d * element size must be a multiple of 16 bytes, d <= 128.
+ *
+ * moda_paged_append — appends the new tokens' keys and values, with the
+ * position rotation applied on the way, and rotates the queries: for a token
+ * at position p, every q and k head row x becomes, over the pairs
+ * j < rot_dim/2 with c = rope[p][j], s = rope[p][rot_dim/2 + j],
+ *     (x1, x2) -> (x1 c - x2 s, x2 c + x1 s),
+ *     pair j = features (j, j + rot_dim/2), or (2j, 2j+1) if interleaved != 0;
+ * features past rot_dim, and v, are copied. Each product and sum is one IEEE
+ * fp32 operation; the result is rounded once to the output type.
+ *   q [N,Hq,d], k, v [N,Hkv,d]  in   heads dense, q_stride / k_stride /
+ *                                    v_stride elements from token to token
+ *                                    (>= heads * d, multiples of 16 bytes), so
+ *                                    column blocks of one projection's output
+ *                                    serve as they are. q may be NULL.
+ *   rope [rope_len, rot_dim] fp32 in cos | sin rows by position, or NULL: no
+ *                                    rotation. rot_dim even, 0 < rot_dim <= d.
+ *   k_pages, v_pages            out  row p % page_size of the position's page
+ *   q_out [N,Hq,d]              out  NULL iff q is
+ *   kd, vd [N,Ld,Hkv,d]         out  optional (both or neither): the rotated k
+ *                                    and the v also go to slot `slot` of the
+ *                                    token's depth rows, the write step that
+ *                                    moda_depth_write does as a separate pass.
+ *                                    q and depth k share the token's position,
+ *                                    so rotated with rotated gives the same
+ *                                    logit as neither.
+ * A token with a negative position, or one that rope does not reach, is
+ * skipped: nothing of it is written. A token without a page still gets its
+ * q_out and depth rows. A page a call writes to must belong to one sequence
+ * and stand once in its table; else which token's values it ends up with is
+ * undefined.
+ *
+ * moda_paged_append_q8 — the same into 8-bit pages. For each page, kv-head and
+ * tensor: 2^e is the smallest power of two (e >= -126) with amax <= 127 * 2^e,
+ * amax the largest finite |x| among the rows this call writes there (0 if they
+ * are all zero). If the page holds earlier tokens of the sequence (the first
+ * row written is not row 0) the new scale is max(old scale, 2^e) and earlier
+ * codes become round-half-even(code * old / new); else it is 2^e. New codes
+ * are round-half-even(x / scale) of the fp32 (rotated) values, clamped to
+ * +-127; NaN gives 0, an infinity +-127. q_out, kd, vd as above.
+ *
+ * Errors: MODA_ERR_INVALID_VALUE (NULL, sizes < 1, Hq % Hkv, slot outside
+ * [0, Ld), rot_dim odd or outside [1, d], strides too small),
+ * MODA_ERR_MISALIGNED, MODA_ERR_UNSUPPORTED (d).
+ */
+moda_status moda_paged_append(const void* q, const void* k, const void* v,
+                              long long q_stride, long long k_stride, long long v_stride,
+                              const float* rope, int rope_len, int rot_dim, int interleaved,
+                              const int32_t* cu_q, const int32_t* ctx_lens, const int32_t* block_table,
+                              int N, int B, int Hq, int Hkv, int d,
+                              int num_pages, int page_size, int max_blocks, moda_dtype dtype,
+                              void* k_pages, void* v_pages, void* q_out,
+                              void* kd, void* vd, int Ld, int slot, void* stream);
+moda_status moda_paged_append_q8(const void* q, const void* k, const void* v,
+                                 long long q_stride, long long k_stride, long long v_stride,
+                                 const float* rope, int rope_len, int rot_dim, int interleaved,
+                                 const int32_t* cu_q, const int32_t* ctx_lens, const int32_t* block_table,
+                                 int N, int B, int Hq, int Hkv, int d,
+                                 int num_pages, int page_size, int max_blocks, moda_dtype dtype,
+                                 int8_t* k_pages, int8_t* v_pages, float* k_scale, float* v_scale,
+                                 void* q_out, void* kd, void* vd, int Ld, int slot, void* stream);
+
+/*
+ * moda_fwd_paged — the read step over the paged cache: for a new token at
+ * position p of sequence b and query head h (kv-head g = h / G), ONE softmax
+ * over the sequence keys j = 0..p that have a page, and the token's own depth
+ * keys, slots 0..Ld-1 of kd[i]:
+ *   out[i,h] = sum_j P_j v_j + sum_x P'_x vd[i,x,g],  lse[i,h] = log of the
+ *   softmax's denominator. A row that sees nothing (Ld = 0 and no position or
+ *   no page) gets zeros and lse = -inf. Keys a row does not see never reach
+ *   it, whatever they hold (NaN and infinities included).
+ *   q, out [N,Hq,d]; lse [N,Hq] fp32 (may be NULL); kd, vd [N,Ld_cap,Hkv,d]
+ *   with Ld <= Ld_cap slots in use (NULL iff Ld == 0).
+ *   max_q      in  about the most new tokens any sequence has; it only selects
+ *                  the kernel, results do not depend on its being right
+ *   workspace  in  device scratch of >= moda_fwd_paged_workspace_bytes(...),
+ *                  16-byte aligned, contents on entry ignored (may be NULL
+ *                  when that is 0). Calls that share it must not overlap.
+ * The attention does not append: call moda_paged_append first, with the same
+ * cu_q, ctx_lens and block_table. moda_fwd_paged_q8 reads 8-bit pages; depth
+ * rows stay in `dtype`. bf16 with d % 8 == 0 and page_size % 16 == 0 runs on
+ * the tensor cores, everything else on the SIMT kernels (MODA_IMPL_TC2 is not
+ * offered: MODA_ERR_UNSUPPORTED). Errors otherwise as moda_fwd_ex.
+ */
+size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d, moda_dtype dtype);
+moda_status moda_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
+                           const void* kd, const void* vd,
+                           const int32_t* cu_q, const int32_t* ctx_lens, const int32_t* block_table,
+                           int N, int B, int max_q, int Hq, int Hkv, int d, int Ld, int Ld_cap,
+                           int num_pages, int page_size, int max_blocks, moda_dtype dtype, float scale,
+                           void* out, float* lse, void* workspace, size_t workspace_bytes,
+                           void* stream, moda_impl impl);
+moda_status moda_fwd_paged_q8(const void* q, const int8_t* k_pages, const int8_t* v_pages,
+                              const float* k_scale, const float* v_scale,
+                              const void* kd, const void* vd,
+                              const int32_t* cu_q, const int32_t* ctx_lens, const int32_t* block_table,
+                              int N, int B, int max_q, int Hq, int Hkv, int d, int Ld, int Ld_cap,
+                              int num_pages, int page_size, int max_blocks, moda_dtype dtype, float scale,
+                              void* out, float* lse, void* workspace, size_t workspace_bytes,
+                              void* stream, moda_impl impl);
+
 /* moda_fwd reading depth keys/values from moda_pack_depth's layout. */
 moda_status moda_fwd_packed(const void* q, const void* k, const void* v,
                             const void* packed_depth,

@@ -1,0 +1,242 @@
+"""GPU parity of the attention over the paged cache (moda_fwd_paged,
+moda_fwd_paged_q8) with the float64 oracle, by bounds that follow from the
+arithmetic (paged_util.check_rows). Everything a row must not see holds NaN."""
+import pytest
+import torch
+
+import oracle
+from paged_util import Paged, check_rows, make
+
+pytestmark = pytest.mark.gpu
+
+moda = pytest.importorskip("depth_kv_attention_b200")
+
+
+def steps(*ctx):
+    return tuple((c, 1) for c in ctx)
+
+
+CASES = [
+    Paged("one_key", steps(1)),
+    Paged("one_key_depth", steps(1), Ld=3, cap=3),
+    Paged("tails", steps(*range(1, 35)), Hq=4, Hkv=1, Ld=2, cap=5),
+    Paged("mixed", steps(700, 3, 64, 65, 129, 1024, 333), Hq=32, Hkv=4, Ld=28, cap=28),
+    Paged("long", steps(5000), Hq=8, Hkv=1, Ld=4, cap=4, P=64),
+    Paged("g1", steps(100, 257), Hq=4, Hkv=4, Ld=5, cap=8),
+    Paged("g7", steps(100, 257), Hq=14, Hkv=2, Ld=5, cap=5, P=48),
+    Paged("g16", steps(90, 31), Hq=16, Hkv=1, P=32),
+    Paged("g20", steps(90, 31), Hq=20, Hkv=1, P=32, Ld=17, cap=17),
+    Paged("g32", steps(200, 77), Hq=32, Hkv=1, Ld=28, cap=33, P=32),
+    Paged("g71", steps(100), Hq=71, Hkv=1, Ld=1, cap=1),
+    Paged("d64", steps(130, 40), d=64, Ld=4, cap=4),
+    Paged("d96", steps(130, 40), d=96, Ld=4, cap=4, P=128),
+    Paged("d8", steps(130, 40), d=8, Hq=6, Hkv=2),
+    Paged("d72", steps(130, 40), d=72, Hq=6, Hkv=2, Ld=9, cap=9),
+    Paged("draft", ((300, 4), (65, 5), (20, 0), (130, 3)), Hq=8, Hkv=2, Ld=6, cap=6, spare_rows=2),
+    Paged("draft_g32", ((300, 4), (64, 4)), Hq=32, Hkv=1, Ld=20, cap=28, P=32),
+    Paged("chunk", ((200, 100), (130, 130), (64, 1)), Hq=8, Hkv=2, Ld=3, cap=3),
+    Paged("chunk_g8", ((700, 300), (90, 33)), Hq=8, Hkv=1, Ld=16, cap=16, P=64),
+    Paged("chunk_g1", ((300, 150),), Hq=2, Hkv=2, Ld=7, cap=7, d=128),
+    Paged("chunk_g7", ((300, 90),), Hq=7, Hkv=1, Ld=2, cap=2, d=96),
+    Paged("deep", steps(40), Hq=4, Hkv=1, Ld=130, cap=140),
+    Paged("short_ctx", ((2, 5), (0, 1), (3, 3)), Hq=8, Hkv=2),
+    Paged("short_ctx_depth", ((2, 5), (0, 1), (3, 3)), Hq=8, Hkv=2, Ld=3, cap=3),
+    Paged("odd_page", steps(100, 33), P=24, Ld=2, cap=2),
+    Paged("page1", steps(20, 7), P=1, d=16, Hq=2, Hkv=1),
+    Paged("f32", ((128, 1), (70, 3), (300, 1)), Hq=4, Hkv=1, d=64, Ld=4, cap=4, dtype="f32"),
+    Paged("f32_d72", ((50, 2), (9, 9)), Hq=6, Hkv=3, d=72, P=5, Ld=3, cap=4, dtype="f32"),
+    Paged("f32_d128", steps(400, 1), Hq=8, Hkv=1, d=128, P=64, dtype="f32"),
+    Paged("many", tuple((1 + b % 70, b % 3) for b in range(1100)), d=32, Hq=2, Hkv=1, Ld=1, cap=1),
+]
+
+
+def run(x, c, q8, impl="auto", **kw):
+    if q8:
+        return moda.moda_fwd_paged_q8(x["q"], x["k_pages"], x["v_pages"], x["k_scale"], x["v_scale"], x["table"],
+                                      x["cu_q"], x["ctx"], x["max_q"], kd=x["kd"], vd=x["vd"], Ld=c.Ld, impl=impl, **kw)
+    return moda.moda_fwd_paged(x["q"], x["k_pages"], x["v_pages"], x["table"], x["cu_q"], x["ctx"], x["max_q"],
+                               kd=x["kd"], vd=x["vd"], Ld=c.Ld, impl=impl, **kw)
+
+
+def want(x, c):
+    return oracle.paged_forward(x["q"], x["k_pages"], x["v_pages"], x["table"], x["cu_q"], x["ctx"], x["kd"], x["vd"],
+                                c.Ld, c.d ** -0.5, x.get("k_scale"), x.get("v_scale"))
+
+
+def keys_of(c):
+    return max(n for n, _ in c.seqs) + c.Ld
+
+
+def cuda(x):
+    return {n: t.cuda() if torch.is_tensor(t) else t for n, t in x.items()}
+
+
+@pytest.mark.parametrize("impl", ["auto", "simt"])
+@pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
+@pytest.mark.parametrize("c", CASES, ids=[c.name for c in CASES])
+def test_parity(c, q8, impl):
+    x = make(c, q8=q8)
+    # rows behind the last sequence stay as they were
+    out = torch.full((c.N, c.Hq, c.d), 9.0, dtype=x["q"].dtype, device="cuda")
+    lse = torch.full((c.N, c.Hq), 9.0, device="cuda")
+    got = run(cuda(x), c, q8, impl, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert moda.moda_device_status() == 0
+    assert got[0] is out and got[1] is lse
+    check_rows(out, lse, want(x, c), c.dtype, keys_of(c), c.d, c.name)
+    n = c.N - c.spare_rows
+    assert torch.all(out[n:] == 9) and torch.all(lse[n:] == 9)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
+def test_peaked_logits(q8):
+    """Queries of large norm: one key takes nearly all the weight, running
+    maxima jump, and far keys underflow."""
+    c = Paged("peak", ((600, 1), (200, 3)), Hq=16, Hkv=2, Ld=5, cap=5)
+    x = make(c, q8=q8)
+    x["q"] = x["q"] * 12
+    got = run(cuda(x), c, q8)
+    torch.cuda.synchronize()
+    check_rows(*got, want(x, c), c.dtype, keys_of(c), c.d)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
+def test_pages_that_are_not_there(q8):
+    """Holes in the table (an id below 0 or past the pool, whole tiles of them
+    too) and a table shorter than the context: those positions are not seen."""
+    c = Paged("holes", ((400, 2), (300, 1), (500, 1)), Hq=8, Hkv=2, Ld=2, cap=2)
+    x = make(c, q8=q8)
+    x["table"][0, 3], x["table"][0, 24], x["table"][1, 0:16] = -1, 10 ** 6, -7
+    x["table"][2, :] = -1
+    x["table"] = x["table"][:, :28].contiguous()
+    got = run(cuda(x), c, q8)
+    torch.cuda.synchronize()
+    check_rows(*got, want(x, c), c.dtype, keys_of(c), c.d)
+
+
+def test_nan_where_a_row_does_not_look():
+    """NaN and infinities in the values and keys of a later new token and in
+    another token's depth rows reach only the rows that see them."""
+    c = Paged("nan", ((70, 4),), Hq=8, Hkv=1, Ld=3, cap=3)
+    x = make(c)
+    clean = want(x, c)
+    page, row = int(x["table"][0, 69 // 16]), 69 % 16   # the last token's key and value
+    x["k_pages"][page, :, row], x["v_pages"][page, :, row] = float("nan"), float("inf")
+    x["vd"][2, 1], x["kd"][2, 0] = float("nan"), float("inf")
+    out, lse = run(cuda(x), c, False)
+    torch.cuda.synchronize()
+    ok = [0, 1]
+    check_rows(out[ok], lse[ok], tuple(w[ok] for w in clean), c.dtype, keys_of(c), c.d)
+    assert torch.isnan(out[2:]).all() and torch.isnan(lse[3]).all()
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
+def test_twice_the_same_and_shared_workspace(q8):
+    """The same call twice gives the same bits, also through a workspace that
+    holds NaN; two captured graphs that share it replay one after the other."""
+    c = Paged("again", ((3000, 1), (1500, 2), (10, 1)), Hq=32, Hkv=4, Ld=6, cap=6)
+    x = cuda(make(c, q8=q8))
+    n = moda.moda_fwd_paged_workspace_bytes(c.N, len(c.seqs), x["max_q"], c.Hq, c.Hkv, c.d, torch.bfloat16)
+    ws = torch.full((max(n, 16) // 4,), float("nan"), device="cuda").view(torch.uint8)
+    a = run(x, c, q8)
+    b = run(x, c, q8, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    y = dict(x, q=x["q"] * 2)
+    wanted = [a, run(y, c, q8)]
+    graphs, outs = [], []
+    for t in (x, y):
+        outs.append([torch.empty_like(a[0]), torch.empty_like(a[1])])
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            run(t, c, q8, workspace=ws, out=outs[-1][0], lse=outs[-1][1])
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, wanted):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+
+
+def test_graph_follows_the_lengths():
+    """A captured decode step serves later steps: only device arrays change."""
+    c = Paged("replay", ((200, 1), (90, 1)), Hq=8, Hkv=1, Ld=2, cap=2)
+    x = make(c)
+    x["k_pages"], x["v_pages"] = torch.nan_to_num(x["k_pages"], nan=0.5), torch.nan_to_num(x["v_pages"], nan=0.5)
+    g = cuda(x)
+    out, lse = torch.empty_like(g["q"]), torch.empty((c.N, c.Hq), device="cuda")
+    run(g, c, False, out=out, lse=lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(g, c, False, out=out, lse=lse)
+    for ctx in ((200, 90), (201, 1), (16, 96), (0, 33)):
+        x["ctx"] = torch.tensor(ctx, dtype=torch.int32)
+        g["ctx"].copy_(x["ctx"])
+        graph.replay()
+        torch.cuda.synchronize()
+        check_rows(out, lse, want(x, c), c.dtype, keys_of(c), c.d, str(ctx))
+
+
+def test_other_stream():
+    c = Paged("stream", ((900, 1), (90, 1)), Hq=32, Hkv=4, Ld=2, cap=2)
+    x = cuda(make(c))
+    a = run(x, c, False)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    b = run(x, c, False, stream=side, out=torch.empty_like(x["q"]))
+    side.synchronize()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_max_q_is_a_hint():
+    """Any max_q gives the oracle's rows (it only selects the kernel)."""
+    c = Paged("hint", ((150, 40), (33, 1)), Hq=8, Hkv=1, Ld=2, cap=2)
+    x = make(c)
+    w = want(x, c)
+    for m in (1, 3, 17, 1000):
+        got = run(dict(cuda(x), max_q=m), c, False)
+        torch.cuda.synchronize()
+        check_rows(*got, w, c.dtype, keys_of(c), c.d, str(m))
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
+def test_layers_of_steps(q8):
+    """As they are used together: per step and layer append (rotated, and into
+    the layer's depth slot), then attend to the cache and the slots of the
+    layers before; prompts first, then single tokens. Every attention call
+    matches the oracle on the cache that the calls before it left."""
+    Hq, Hkv, d, P, layers = 8, 2, 64, 16, 3
+    g = torch.Generator("cpu")
+    g.manual_seed(5)
+    pages = 12
+    table = torch.randperm(pages, generator=g)[:8].view(2, 4).to(torch.int32).cuda()
+    f = 10000.0 ** (-torch.arange(0, d, 2, dtype=torch.float64) / d)
+    a = torch.arange(64, dtype=torch.float64)[:, None] * f
+    rope = torch.cat([a.cos(), a.sin()], 1).float().cuda()
+    kv = torch.int8 if q8 else torch.bfloat16
+    cache = [[torch.zeros(pages, Hkv, P, d, dtype=kv, device="cuda") for _ in range(2)] for _ in range(layers)]
+    scale = [[torch.zeros(pages, Hkv, device="cuda") for _ in range(2)] for _ in range(layers)]
+    ctx = [0, 0]
+    for new in ((21, 14), (1, 1), (1, 1), (2, 0), (1, 3)):
+        N = sum(new)
+        ctx = [c + n for c, n in zip(ctx, new)]
+        cu = torch.tensor([0, new[0], N], dtype=torch.int32).cuda()
+        lens = torch.tensor(ctx, dtype=torch.int32).cuda()
+        kd = torch.full((N, layers, Hkv, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+        vd = kd.clone()
+        for layer in range(layers):
+            q, k, v = (torch.randn(N, h, d, generator=g).to(torch.bfloat16).cuda() for h in (Hq, Hkv, Hkv))
+            pg, sc = cache[layer], scale[layer]
+            kw = dict(rope=rope, kd=kd, vd=vd, slot=layer)
+            if q8:
+                qr = moda.moda_paged_append_q8(q, k, v, *pg, *sc, table, cu, lens, **kw)
+                out, lse = moda.moda_fwd_paged_q8(qr, *pg, *sc, table, cu, lens, max(new), kd=kd, vd=vd, Ld=layer)
+            else:
+                qr = moda.moda_paged_append(q, k, v, *pg, table, cu, lens, **kw)
+                out, lse = moda.moda_fwd_paged(qr, *pg, table, cu, lens, max(new), kd=kd, vd=vd, Ld=layer)
+            torch.cuda.synchronize()
+            w = oracle.paged_forward(qr, *pg, table.cpu(), cu.cpu(), lens.cpu(), kd, vd, layer, d ** -0.5,
+                                     *(sc if q8 else (None, None)))
+            check_rows(out, lse, w, "bf16", max(ctx) + layer, d)
+            turned = oracle.rotate(k[0].double().cpu().numpy(), rope[ctx[0] - new[0]].double().cpu().numpy(), False)
+            assert abs(kd[0, layer].double().cpu().numpy() - turned).max() <= 2.0 ** -8 * abs(turned).max() + 1e-5
