@@ -601,9 +601,12 @@ moda_status run_fwd_paged(const void* q, const void* k_pages, const void* v_page
     a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.k_scale = k_scale; a.v_scale = v_scale;
     a.kd = kd; a.vd = vd; a.Hq = Hq; a.G = Hq / Hkv; a.Ld = Ld; a.Ld_cap = Ld_cap; a.max_q = max_q;
     a.scale = scale; a.dtype = dtype; a.out = out; a.lse = lse; a.workspace = workspace;
-    if (impl == MODA_IMPL_TC || impl == MODA_IMPL_TC2) return MODA_ERR_UNSUPPORTED;
+    const bool tc_ok = paged_dec_supported(a);
+    if (impl == MODA_IMPL_TC2 || (impl == MODA_IMPL_TC && !tc_ok)) return MODA_ERR_UNSUPPORTED;
     if (status_ptr(&a.status, &a.wait_limit) != cudaSuccess) return MODA_ERR_CUDA;
-    return launch_paged_fwd_simt(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MODA_OK : MODA_ERR_LAUNCH;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = tc_ok && impl != MODA_IMPL_SIMT ? launch_paged_dec(a, s) : launch_paged_fwd_simt(a, s);
+    return e == cudaSuccess ? MODA_OK : MODA_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -632,8 +635,8 @@ moda_status moda_paged_append_q8(const void* q, const void* k, const void* v, lo
 }
 
 size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d, moda_dtype dtype) {
-    (void)N; (void)B; (void)max_q; (void)Hq; (void)Hkv; (void)d; (void)dtype;
-    return 0;
+    if (N < 1 || B < 1 || max_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1 || d > 128) return 0;
+    return dtype == MODA_BF16 ? paged_dec_workspace(max_q, Hq / Hkv, d) : 0;
 }
 
 moda_status moda_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* kd, const void* vd,

@@ -62,6 +62,11 @@ struct PagedFwdArgs {
 };
 
 cudaError_t launch_paged_append(const AppendArgs& a, cudaStream_t s);
+// Tensor-core attention for few rows per sequence (moda_paged_dec_sm100.cu).
+bool paged_dec_supported(const PagedFwdArgs& a);
+size_t paged_dec_workspace(int max_q, int G, int d);
+cudaError_t launch_paged_dec(const PagedFwdArgs& a, cudaStream_t s);
+// Every shape (moda_paged_simt.cu).
 cudaError_t launch_paged_fwd_simt(const PagedFwdArgs& a, cudaStream_t s);
 
 }  // namespace moda

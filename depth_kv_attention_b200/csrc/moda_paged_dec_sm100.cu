@@ -1,0 +1,957 @@
+// Attention over the paged sequence cache for few query rows per sequence
+// (decode, drafted tokens, ragged mixes): bf16 or 8-bit pages, d <= 128.
+//
+// What it computes: one softmax over the sequence keys a new token sees and
+// its own depth keys ("动态混合深度注意力机制MoDA技术解析", mhpn.cn, §1.2 formula,
+// §2.2 online-softmax state and dual mask), all heads of a GQA group together.
+//
+// What bounds it: a token's G rows share every key, so a step reads K and V
+// once and does 4 G d operations per key and head: memory-bound up to about
+// G * tokens = 64. The design keeps loads in flight and everything else out of
+// the way:
+//  * The stages of all units (paged_units.cuh) are cut into equal parts, two
+//    CTAs per SM; cut units leave (m, l, O) in the workspace and a small
+//    second kernel joins them in a fixed order.
+//  * One producer warp fills a ring of 64-key K and V slots by TMA, one box of
+//    16 rows per page slice, so any page size that is a multiple of 16 works;
+//    page ids and scales are fetched 32 slices at a time, one batch ahead.
+//  * Four consumer warps. With up to 16 rows each takes its own 16 keys of a
+//    stage (own softmax state, joined at the unit's end); with 32 or 64 rows
+//    two or four of them take 16 rows each of the same keys. The products are
+//    mma.sync m16n8k16: 16 rows are all a decode step has, where a tcgen05
+//    tile would be 128 rows high, seven eighths of them padding.
+//  * 8-bit pages: a lane reads whole 16-byte pieces of a row and turns codes
+//    into bf16 exactly, two at a time ((0x4300 | low 7 bits) is 128 + them, and
+//    (0x4300 | sign bit) is 128 or 256, so one subtraction gives the code). The
+//    order in which a lane holds features is free in a product's contracted
+//    index (queries are laid out alike) and only permutes the output columns.
+//    A key's scale multiplies its logit, a value's scale its P: both exact, as
+//    scales are powers of two.
+//  * Rounding: logits, P, l, O in fp32; P is rounded to bf16 as the operand of
+//    P V (l sums the unrounded P).
+//  * A value that a row must not see may be anything: a masked P is exactly 0,
+//    but 0 * NaN is not. Stages in which some row is masked look for
+//    non-finite values, add those to the rows that do see them on the CUDA
+//    cores and clear them before the product.
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "paged_units.cuh"
+#include "sm100_ptx.cuh"
+#include "tmap_host.h"
+
+namespace moda {
+namespace {
+
+constexpr int kConsumers = 4;                   // consumer warps
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kProducer = kConsumers;
+constexpr int kSliceRows = 16;
+constexpr float kLazy = 8.f;                    // log2 units before a running max moves
+
+struct DecParams {
+    CUtensorMap tm_k, tm_v, tm_kd, tm_vd;
+    PagedCache c;
+    const __nv_bfloat16* q;
+    const float* k_scale;
+    const float* v_scale;
+    __nv_bfloat16* out;
+    float* lse;
+    float* part_o;   // [2W][MR][D]
+    float* part_ml;  // [2W][MR][2]
+    int4* desc;      // [W]: {sequence, kv-head, tile, parts}, parts = 0: none
+    int Hq, G, Ld, DSL, W, min_stages;
+    float sl2;
+    unsigned int* status;
+    unsigned int wait_limit;
+};
+
+template <bool Q8, int NH, int WR>
+struct Cfg {
+    static constexpr int D = 64 * NH;
+    static constexpr int MR = 16 * WR;
+    static constexpr int WK = kConsumers / WR;               // warps that share a stage's keys
+    static constexpr int SL = WR;                            // slices of a stage per warp
+    static constexpr int kSeqSlice = Q8 ? 2048 : 2048 * NH;  // bytes of 16 keys
+    static constexpr int kDepSlice = 2048 * NH;
+    static constexpr int kSlot = 4 * kSeqSlice;
+    static constexpr int DS = kSlot / kDepSlice;             // depth slices per stage
+    static constexpr int NS = Q8 || NH == 1 ? 8 : 5;         // ring slots
+    static constexpr int kMerge = WK == 1 ? 0 : 2 * 16 * D * 4;
+    static constexpr int kSmem = 1024 + NS * kSlot + kMerge + 1024;
+};
+
+struct __align__(8) DecBars {
+    uint64_t full[8], empty[8];
+    float scale[8][4];   // per slot and slice: scale (1 for bf16), -1: no page
+    float ml[kConsumers][16][2];
+    long long scan[kThreads / 32];
+    long long begin_in_seq;
+    long long total, before;
+    int begin_seq;
+    int abort_flag;
+};
+static_assert(sizeof(DecBars) <= 1024, "barrier block");
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+// Two int8 codes, in bytes 0 and 2 of w, as a bf16 pair (exact).
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t w) {
+    const uint32_t y = (w & 0x007f007fu) | 0x43004300u, base = (w & 0x00800080u) | 0x43004300u;
+    __nv_bfloat162 a, b;
+    memcpy(&a, &y, 4);
+    memcpy(&b, &base, 4);
+    const __nv_bfloat162 r = __hsub2(a, b);
+    uint32_t o;
+    memcpy(&o, &r, 4);
+    return o;
+}
+
+// Byte address of feature f of row r of a bf16 slice (64-feature halves of 16
+// rows, 128-byte swizzle).
+__device__ __forceinline__ uint32_t bf16_at(uint32_t slice, int r, int f) {
+    return slice + (f >> 6) * 2048 + r * 128 + ((((f >> 3) & 7) ^ (r & 7)) << 4) + (f & 7) * 2;
+}
+
+// The K operand of one 16-key slice, 8 keys j at a time: S += Q K^T.
+template <int NH>
+__device__ __forceinline__ void qk_bf16(uint32_t slice, const uint32_t (&qf)[NH * 4][4], float (&s)[2][4], int lane) {
+    const int r = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
+#pragma unroll
+    for (int k = 0; k < NH * 4; ++k) {
+        uint32_t b[4];
+        ldsm4(bf16_at(slice, r, 16 * k + 8 * hi), b);
+        mma_bf16(s[0], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[0], b[1]);
+        mma_bf16(s[1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[2], b[3]);
+    }
+}
+// O += P V, output tile nt = features 8 nt .. 8 nt + 7.
+template <int NH>
+__device__ __forceinline__ void pv_bf16(uint32_t slice, const uint32_t (&pf)[4], float (&o)[NH * 8][4], int lane) {
+    const int r = (lane & 7) + (((lane >> 3) & 1) << 3), hi = lane >> 4;
+#pragma unroll
+    for (int n = 0; n < NH * 4; ++n) {
+        uint32_t b[4];
+        ldsm4t(bf16_at(slice, r, 16 * n + 8 * hi), b);
+        mma_bf16(o[2 * n], pf[0], pf[1], pf[2], pf[3], b[0], b[1]);
+        mma_bf16(o[2 * n + 1], pf[0], pf[1], pf[2], pf[3], b[2], b[3]);
+    }
+}
+
+// 8-bit kernels hold features permuted: lane t of a quad owns features
+// t * D/4 .. of a key row; k-step s takes its features 4s, 4s+2 and 4s+1, 4s+3.
+// Output tile nt, column n = feature n * D/8 + nt.
+template <int NH>
+__device__ __forceinline__ void qk_q8(uint32_t slice, const uint32_t (&qf)[NH * 4][4], float (&s)[2][4], int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t row = slice + (8 * j + g) * 128;
+#pragma unroll
+        for (int c = 0; c < NH; ++c) {  // 16 codes = 4 k-steps
+            const uint4 w = lds128(row + (((t * NH + c) ^ g) << 4));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int k = 4 * c + e;
+                mma_bf16(s[j], qf[k][0], qf[k][1], qf[k][2], qf[k][3], codes_to_bf16(ww[e]), codes_to_bf16(ww[e] >> 8));
+            }
+        }
+    }
+}
+template <int NH>
+__device__ __forceinline__ void pv_q8(uint32_t slice, const uint32_t (&pf)[4], float (&o)[NH * 8][4], int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t w[4][NH * 2];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int r = 2 * t + (x & 1) + 8 * (x >> 1);
+        if (NH == 2) {
+            const uint4 v = lds128(slice + r * 128 + ((g ^ (r & 7)) << 4));
+            w[x][0] = v.x; w[x][1] = v.y; w[x][NH * 2 - 2] = v.z; w[x][NH * 2 - 1] = v.w;
+        } else {
+            const uint2 v = lds64(slice + r * 128 + (((g >> 1) ^ (r & 7)) << 4) + (g & 1) * 8);
+            w[x][0] = v.x; w[x][1] = v.y;
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NH * 8; ++nt) {
+        const uint32_t sel = 0x4400u + (uint32_t)(nt & 3) * 0x1111u;  // byte nt%4 of each row, at bytes 0 and 2
+        const uint32_t b0 = codes_to_bf16(__byte_perm(w[0][nt >> 2], w[1][nt >> 2], sel));
+        const uint32_t b1 = codes_to_bf16(__byte_perm(w[2][nt >> 2], w[3][nt >> 2], sel));
+        mma_bf16(o[nt], pf[0], pf[1], pf[2], pf[3], b0, b1);
+    }
+}
+// bf16 depth slices in the same permuted order.
+template <int NH>
+__device__ __forceinline__ void qk_bf16_perm(uint32_t slice, const uint32_t (&qf)[NH * 4][4], float (&s)[2][4], int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int c = 0; c < NH * 2; ++c) {  // 8 features = 2 k-steps
+            const uint4 w = lds128(bf16_at(slice, 8 * j + g, t * 16 * NH + 8 * c));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t lo = e ? w.z : w.x, hi = e ? w.w : w.y;
+                const int k = 2 * c + e;
+                mma_bf16(s[j], qf[k][0], qf[k][1], qf[k][2], qf[k][3], __byte_perm(lo, hi, 0x5410),
+                         __byte_perm(lo, hi, 0x7632));
+            }
+        }
+}
+template <int NH>
+__device__ __forceinline__ void pv_bf16_perm(uint32_t slice, const uint32_t (&pf)[4], float (&o)[NH * 8][4], int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int c = 0; c < NH; ++c) {  // 8 of the lane's 8 NH columns
+        uint32_t w[4][4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const uint4 v = lds128(bf16_at(slice, 2 * t + (x & 1) + 8 * (x >> 1), g * 8 * NH + 8 * c));
+            w[x][0] = v.x; w[x][1] = v.y; w[x][2] = v.z; w[x][3] = v.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
+            mma_bf16(o[8 * c + e], pf[0], pf[1], pf[2], pf[3], __byte_perm(w[0][e >> 1], w[1][e >> 1], sel),
+                     __byte_perm(w[2][e >> 1], w[3][e >> 1], sel));
+        }
+    }
+}
+
+// Feature of element (nt, c) of a lane's output fragment.
+template <bool Q8, int NH>
+__device__ __forceinline__ int out_col(int nt, int c, int t) {
+    return Q8 ? (2 * t + c) * (8 * NH) + nt : 8 * nt + 2 * t + c;
+}
+
+// Keys of a bf16 slice with a non-finite value, as a 16-bit mask.
+template <int NH>
+__device__ __forceinline__ uint32_t nonfinite_keys(uint32_t slice, int lane) {
+    bool bad = false;
+    const int r = lane >> 1;
+#pragma unroll
+    for (int x = 0; x < NH * 4; ++x) {
+        const uint4 v = lds128(slice + (x >> 2) * 2048 + r * 128 + (((lane & 1) * 4 + (x & 3)) << 4));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            bad |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+    }
+    const uint32_t b = __ballot_sync(0xffffffffu, bad);
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) m |= ((b >> (2 * k)) & 3u) ? 1u << k : 0u;
+    return m;
+}
+
+// Adds P V of the keys in `bad` to the rows whose P is not 0.
+template <bool Q8, int NH>
+__device__ __forceinline__ void add_nonfinite(uint32_t slice, uint32_t bad, const float (&p)[2][4], float (&o)[NH * 8][4],
+                                              int lane) {
+    for (; bad; bad &= bad - 1) {
+        const int k = __ffs(bad) - 1, src = (lane & ~3) | ((k & 7) >> 1);
+        float pr[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float a = (k & 8) ? ((k & 1) ? p[1][2 * h + 1] : p[1][2 * h]) : ((k & 1) ? p[0][2 * h + 1] : p[0][2 * h]);
+            pr[h] = __shfl_sync(0xffffffffu, a, src);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NH * 8; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint16_t raw;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(bf16_at(slice, k, out_col<Q8, NH>(nt, c, lane & 3))) : "memory");
+                const float v = __uint_as_float((uint32_t)raw << 16);
+                if (pr[0] != 0.f) o[nt][c] += pr[0] * v;
+                if (pr[1] != 0.f) o[nt][2 + c] += pr[1] * v;
+            }
+    }
+}
+template <int NH>
+__device__ __forceinline__ void clear_keys(uint32_t slice, uint32_t bad, int lane) {
+    for (; bad; bad &= bad - 1) {
+        const int k = __ffs(bad) - 1;
+        if (lane < NH * 8)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(slice + (lane >> 3) * 2048 + k * 128 + (lane & 7) * 16), "r"(0) : "memory");
+    }
+}
+
+// Box of 16 rows x 64 bf16 (or 128 codes) into shared memory.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int x, int row, int h, int page) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(ptx::smem_u32(bar)), "r"(x), "r"(row), "r"(h), "r"(page)
+        : "memory");
+}
+
+template <bool Q8, int NH, int WR>
+__global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_constant__ DecParams p) {
+    using C = Cfg<Q8, NH, WR>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* base = smem_raw + (ring - ptx::smem_u32(smem_raw));
+    float* merge = reinterpret_cast<float*>(base + C::NS * C::kSlot);
+    DecBars* bars = reinterpret_cast<DecBars*>(base + C::NS * C::kSlot + C::kMerge);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const PagedCache& c = p.c;
+    const long long max_keys = min((long long)c.max_blocks * c.page_size, 0x7fffffc0LL);
+    const int cta = blockIdx.x;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::NS; ++s) {
+            ptx::mbar_init(&bars->full[s], 1);
+            ptx::mbar_init(&bars->empty[s], kConsumers);
+        }
+        bars->abort_flag = 0;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_smem();
+        p.desc[cta] = make_int4(0, 0, 0, 0);
+    }
+    // ---- the list of stages: each thread sums a run of sequences, then a scan
+    const int per = (c.B + kThreads - 1) / kThreads;
+    const int b0 = min(threadIdx.x * per, c.B), b1 = min(b0 + per, c.B);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += seq_stages<C::MR>(seq_info(c, b), p.G, p.DSL, C::DS, max_keys);
+    long long incl = mine * c.Hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) bars->scan[warp] = incl;
+    __syncthreads();
+    long long total = 0, pre = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) pre += bars->scan[w];
+        total += bars->scan[w];
+    }
+    incl += pre;
+    // parts: at least min_stages stages each
+    const int W = (int)max(1LL, min((long long)p.W, total / p.min_stages));
+    if (cta >= W || total == 0) return;
+    const long long lo = total * cta / W, hi = total * (cta + 1) / W;
+    {
+        long long at = incl - mine * c.Hkv;
+        if (lo >= at && lo < incl) {  // one thread: the CTA's part begins in its run
+            for (int b = b0; b < b1; ++b) {
+                const long long n = seq_stages<C::MR>(seq_info(c, b), p.G, p.DSL, C::DS, max_keys) * c.Hkv;
+                if (lo < at + n) {
+                    bars->begin_seq = b;
+                    bars->begin_in_seq = lo - at;
+                    break;
+                }
+                at += n;
+            }
+        }
+    }
+    __syncthreads();
+    volatile int* abort_flag = &bars->abort_flag;
+    auto fail = [&]() {
+        *abort_flag = 1;
+        atomicOr(p.status, 1u);
+    };
+
+    // ---- the units of this part, walked alike by every warp
+    int b = bars->begin_seq, kvh, rt = 0;
+    long long left = hi - lo;       // stages still to do
+    SeqInfo sq = seq_info(c, b);
+    int first;                      // first stage of the current unit's piece
+    {
+        long long in = bars->begin_in_seq;
+        const long long n = seq_stages<C::MR>(sq, p.G, p.DSL, C::DS, max_keys);
+        kvh = (int)(in / n);
+        in -= (long long)kvh * n;
+        for (;; ++rt) {
+            const int st = unit_shape<C::MR>(sq, rt, p.G, p.DSL, C::DS, max_keys).st;
+            if (in < st) break;
+            in -= st;
+        }
+        first = (int)in;
+    }
+    auto next_unit = [&]() {
+        first = 0;
+        if (++rt * C::MR < sq.n * p.G) return;
+        rt = 0;
+        if (++kvh < c.Hkv) return;
+        kvh = 0;
+        do {
+            sq = seq_info(c, ++b);
+        } while (sq.n == 0 && b + 1 < c.B);  // `left` > 0: a later sequence has stages
+    };
+
+    if (warp == kProducer) {
+        int slot = 0, ph = 1, issued = 0;
+        bool ok = true;
+        while (left > 0) {
+            const UnitShape u = unit_shape<C::MR>(sq, rt, p.G, p.DSL, C::DS, max_keys);
+            const int end = (int)min((long long)u.st, first + left);
+            // page slices [4 first, ...) of the unit, 32 at a time: lane l
+            // holds slice 32 batch + l of the piece; the next batch's page ids
+            // are in flight while this one's boxes are issued
+            const int sl0 = first * 4, sl_all = u.st_seq * 4;
+            auto fetch = [&](int sl) {  // page of slice sl, num_pages: none
+                const int key = sl * kSliceRows;
+                int pg = -1;
+                if (sl < sl_all && key < u.nk) pg = page_of(c, b, key / c.page_size);
+                return pg;
+            };
+            int page = fetch(sl0 + lane), page_next = fetch(sl0 + 32 + lane);
+            float ks = 1.f, vs = 1.f, ks_next = 1.f, vs_next = 1.f;
+            auto scales = [&](int pg, float& a, float& e) {
+                a = pg < 0 ? -1.f : 1.f;
+                e = 1.f;
+                if (Q8 && pg >= 0) {
+                    a = __ldg(p.k_scale + (long long)pg * c.Hkv + kvh);
+                    e = __ldg(p.v_scale + (long long)pg * c.Hkv + kvh);
+                }
+            };
+            scales(page, ks, vs);
+            for (int st = first; st < end; ++st) {
+                const bool seq = st < u.st_seq;
+                const int rel = st * 4 - sl0;
+                if (seq && rel && (rel & 31) == 0) {
+                    page = page_next;
+                    ks = ks_next;
+                    vs = vs_next;
+                    page_next = fetch(sl0 + rel + 32 + lane);
+                }
+                if (seq && (rel & 31) == 16) scales(page_next, ks_next, vs_next);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (ok && !__all_sync(0xffffffffu, ptx::mbar_wait(&bars->empty[slot], ph, p.wait_limit, abort_flag))) {
+                        if (lane == 0) fail();
+                        ok = false;
+                    }
+                    if (ok) {
+                        uint64_t* bar = &bars->full[slot];
+                        const uint32_t dst = ring + slot * C::kSlot;
+                        if (seq) {
+                            const int per_slice = Q8 ? 1 : NH;
+                            const int sl = lane / per_slice, half = lane % per_slice;
+                            const int src = (rel & 31) + (sl & 3);
+                            const int pg = __shfl_sync(0xffffffffu, page, src);
+                            const float sc = __shfl_sync(0xffffffffu, kv ? vs : ks, src);
+                            const float none = __shfl_sync(0xffffffffu, ks, src);
+                            if (lane < 4 * per_slice && half == 0) bars->scale[slot][sl] = none < 0.f ? -1.f : sc;
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, C::kSlot);
+                            __syncwarp();
+                            if (lane < 4 * per_slice) {
+                                const int key = (st * 4 + sl) * kSliceRows;
+                                // a page that is not there lies outside the map: zeros
+                                load_box(dst + sl * C::kSeqSlice + half * 2048, kv ? &p.tm_v : &p.tm_k, bar, half * 64,
+                                         pg < 0 ? 0 : key % c.page_size, kvh, pg < 0 ? c.num_pages : pg);
+                            }
+                        } else {
+                            const int sl = lane / NH, half = lane % NH;
+                            const int x = (st - u.st_seq) * C::DS + sl;
+                            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, C::kSlot);
+                            __syncwarp();
+                            if (lane < C::DS * NH) {
+                                const int tok = p.DSL ? x / p.DSL : 0, sl16 = p.DSL ? x % p.DSL : 0;
+                                const bool in = tok < u.ntok && p.DSL;
+                                load_box(dst + sl * C::kDepSlice + half * 2048, kv ? &p.tm_vd : &p.tm_kd, bar, half * 64, kvh,
+                                         sl16 * kSliceRows, in ? sq.q0 + u.tok0 + tok : c.N);
+                            }
+                        }
+                        ++issued;
+                    }
+                    if (++slot == C::NS) {
+                        slot = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            left -= end - first;
+            if (left > 0) next_unit();
+        }
+        // every copy this CTA issued lands before it exits
+        for (int s = issued > C::NS ? issued - C::NS : 0; s < issued; ++s)
+            ptx::mbar_wait(&bars->full[s % C::NS], (s / C::NS) & 1, 0, nullptr);
+        return;
+    }
+
+    // ------------------------------------------------------ consumer warps
+    const int wr = warp / C::WK, wk = warp % C::WK;  // rows 16 wr .., keys of slices wk, wk + WK, ..
+    const int g = lane >> 2, t = lane & 3;
+    int slot = 0, ph = 0;
+    bool ok = true;
+    while (left > 0) {
+        const UnitShape u = unit_shape<C::MR>(sq, rt, p.G, p.DSL, C::DS, max_keys);
+        const int end = (int)min((long long)u.st, first + left);
+        // this lane's rows g and g + 8 of the warp's 16
+        int tok[2], pos[2];
+        uint32_t qf[NH * 4][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = u.r0 + 16 * wr + g + 8 * h;
+            const bool in = r < u.r0 + u.rows;
+            tok[h] = in ? r / p.G : -1;
+            pos[h] = in ? sq.pos0 + tok[h] : -1;
+            const __nv_bfloat16* row =
+                p.q + ((long long)(sq.q0 + max(tok[h], 0)) * p.Hq + kvh * p.G + (in ? r % p.G : 0)) * c.d;
+#pragma unroll
+            for (int k = 0; k < NH * 4; ++k) {
+                if (Q8) {
+                    const int f = t * 16 * NH + 4 * k;  // features f .. f+3
+                    uint2 w = make_uint2(0, 0);
+                    if (in && f < c.d) w = *reinterpret_cast<const uint2*>(row + f);
+                    qf[k][h] = __byte_perm(w.x, w.y, 0x5410);
+                    qf[k][2 + h] = __byte_perm(w.x, w.y, 0x7632);
+                } else {
+                    const int f = 16 * k + 2 * t;
+                    qf[k][h] = in && f < c.d ? *reinterpret_cast<const uint32_t*>(row + f) : 0u;
+                    qf[k][2 + h] = in && f + 8 < c.d ? *reinterpret_cast<const uint32_t*>(row + f + 8) : 0u;
+                }
+            }
+        }
+        float o[NH * 8][4];
+#pragma unroll
+        for (int n = 0; n < NH * 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+        const int pos_first = sq.pos0 + u.tok0;  // keys up to here are seen by every row of the tile
+        for (int st = first; st < end; ++st) {
+            const bool seq = st < u.st_seq;
+            const int kslot = slot;
+            int kph = ph;
+            if (++slot == C::NS) { slot = 0; ph ^= 1; }
+            const int vslot = slot, vph = ph;
+            if (++slot == C::NS) { slot = 0; ph ^= 1; }
+            if (ok && !__all_sync(0xffffffffu, ptx::mbar_wait(&bars->full[kslot], kph, p.wait_limit, abort_flag))) {
+                if (lane == 0) fail();
+                ok = false;
+            }
+            const uint32_t ka = ring + kslot * C::kSlot, va = ring + vslot * C::kSlot;
+            float s[C::SL][2][4];
+            bool some = !seq || st * 64 + 63 > pos_first;  // some row is masked somewhere in the stage
+            bool part[C::SL];                              // this warp's slice i takes part
+#pragma unroll
+            for (int i = 0; i < C::SL; ++i) {
+                const int sl = wk + i * C::WK;
+                part[i] = seq || sl < C::DS;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][j][e] = 0.f;
+                float ksc = 1.f;
+                if (ok && part[i]) {
+                    if (seq) {
+                        ksc = bars->scale[kslot][sl];
+                        if (Q8) qk_q8<NH>(ka + sl * C::kSeqSlice, qf, s[i], lane);
+                        else qk_bf16<NH>(ka + sl * C::kSeqSlice, qf, s[i], lane);
+                    } else {
+                        if (Q8) qk_bf16_perm<NH>(ka + sl * C::kDepSlice, qf, s[i], lane);
+                        else qk_bf16<NH>(ka + sl * C::kDepSlice, qf, s[i], lane);
+                    }
+                }
+                const float mul = p.sl2 * (Q8 ? ksc : 1.f);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][j][e] *= mul;
+                const int x = (st - u.st_seq) * C::DS + sl;
+                if (!part[i]) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[i][j][e] = -INFINITY;
+                } else if (some || ksc < 0.f) {
+                    const int key0 = (st * 4 + sl) * kSliceRows;
+                    const int dtok = seq || !p.DSL ? 0 : u.tok0 + x / p.DSL, dsl = seq || !p.DSL ? 0 : x % p.DSL * kSliceRows;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = 8 * j + 2 * t + (e & 1), h = e >> 1;
+                            const bool see = seq ? key0 + k <= pos[h] && key0 + k < u.nk && ksc >= 0.f
+                                                 : tok[h] == dtok && dsl + k < p.Ld;
+                            if (!see) s[i][j][e] = -INFINITY;
+                        }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars->empty[kslot]);
+            // ---- online softmax over this warp's keys of the stage
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < C::SL; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[i][j][e]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+            }
+            if (__any_sync(0xffffffffu, mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float mn = fmaxf(m[h], mx[h]);
+                    const float corr = mn == -INFINITY ? 1.f : ptx::ex2(m[h] - mn);
+                    l[h] *= corr;
+                    m[h] = mn;
+#pragma unroll
+                    for (int n = 0; n < NH * 8; ++n) {
+                        o[n][2 * h] *= corr;
+                        o[n][2 * h + 1] *= corr;
+                    }
+                }
+            }
+            const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+            for (int i = 0; i < C::SL; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[i][j][e] = ptx::ex2(s[i][j][e] - ref[e >> 1]);
+                        l[e >> 1] += s[i][j][e];
+                    }
+            if (ok && !__all_sync(0xffffffffu, ptx::mbar_wait(&bars->full[vslot], vph, p.wait_limit, abort_flag))) {
+                if (lane == 0) fail();
+                ok = false;
+            }
+            // ---- values a row must not see may be non-finite (codes are not)
+            if (some && (!Q8 || !seq)) {
+                uint32_t bad[C::SL];
+#pragma unroll
+                for (int i = 0; i < C::SL; ++i) {
+                    const uint32_t sl = va + (wk + i * C::WK) * (seq ? C::kSeqSlice : C::kDepSlice);
+                    bad[i] = 0;
+                    if (ok && part[i]) {
+                        bad[i] = nonfinite_keys<NH>(sl, lane);
+                        if (bad[i]) add_nonfinite<Q8, NH>(sl, bad[i], s[i], o, lane);
+                    }
+                }
+                // warps that share the keys have all read them before they are cleared
+                if (WR > 1) ptx::bar_sync(2, kConsumers * 32); else __syncwarp();
+#pragma unroll
+                for (int i = 0; i < C::SL; ++i)
+                    if (bad[i]) clear_keys<NH>(va + (wk + i * C::WK) * (seq ? C::kSeqSlice : C::kDepSlice), bad[i], lane);
+                ptx::fence_proxy_async_smem();  // before the slot's next copy
+                if (WR > 1) ptx::bar_sync(2, kConsumers * 32); else __syncwarp();
+            }
+#pragma unroll
+            for (int i = 0; i < C::SL; ++i) {
+                const int sl = wk + i * C::WK;
+                if (!ok || !part[i]) continue;
+                float vsc = 1.f;
+                if (Q8 && seq) vsc = fmaxf(bars->scale[vslot][sl], 0.f);
+                uint32_t pf[4];
+                pf[0] = ptx::pack_bf16x2(s[i][0][0] * vsc, s[i][0][1] * vsc);
+                pf[1] = ptx::pack_bf16x2(s[i][0][2] * vsc, s[i][0][3] * vsc);
+                pf[2] = ptx::pack_bf16x2(s[i][1][0] * vsc, s[i][1][1] * vsc);
+                pf[3] = ptx::pack_bf16x2(s[i][1][2] * vsc, s[i][1][3] * vsc);
+                if (seq) {
+                    if (Q8) pv_q8<NH>(va + sl * C::kSeqSlice, pf, o, lane);
+                    else pv_bf16<NH>(va + sl * C::kSeqSlice, pf, o, lane);
+                } else {
+                    if (Q8) pv_bf16_perm<NH>(va + sl * C::kDepSlice, pf, o, lane);
+                    else pv_bf16<NH>(va + sl * C::kDepSlice, pf, o, lane);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars->empty[vslot]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
+        // ---- join the warps that shared the rows: upper half into lower half
+        if (C::WK > 1) {
+#pragma unroll
+            for (int half = C::WK / 2; half >= 1; half /= 2) {
+                ptx::bar_sync(1, kConsumers * 32);  // the buffers are free
+                const int buf = wr * (C::WK / 2 > 1 ? C::WK / 2 : 1) + wk % half;
+                float* mo = merge + buf * 16 * C::D;
+                if (wk >= half && wk < 2 * half) {
+#pragma unroll
+                    for (int n = 0; n < NH * 8; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mo[(n * 4 + e) * 32 + lane] = o[n][e];
+                    if (t == 0) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            bars->ml[buf][g + 8 * h][0] = m[h];
+                            bars->ml[buf][g + 8 * h][1] = l[h];
+                        }
+                    }
+                }
+                ptx::bar_sync(1, kConsumers * 32);
+                if (wk < half) {
+                    float c1[2], c2[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float m2 = bars->ml[buf][g + 8 * h][0], l2 = bars->ml[buf][g + 8 * h][1];
+                        const float mn = fmaxf(m[h], m2), rf = mn == -INFINITY ? 0.f : mn;
+                        c1[h] = ptx::ex2(m[h] - rf);
+                        c2[h] = ptx::ex2(m2 - rf);
+                        l[h] = l[h] * c1[h] + l2 * c2[h];
+                        m[h] = mn;
+                    }
+#pragma unroll
+                    for (int n = 0; n < NH * 8; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[n][e] = o[n][e] * c1[e >> 1] + mo[(n * 4 + e) * 32 + lane] * c2[e >> 1];
+                }
+            }
+        }
+        const bool whole = first == 0 && end == u.st;
+        if (wk == 0) {
+            if (whole) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (tok[h] < 0) continue;
+                    const int r = u.r0 + 16 * wr + g + 8 * h;
+                    const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
+                    const long long row = (long long)(sq.q0 + tok[h]) * p.Hq + kvh * p.G + r % p.G;
+                    __nv_bfloat16* dst = p.out + row * c.d;
+                    if (Q8) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int f0 = out_col<true, NH>(0, e, t);
+#pragma unroll
+                            for (int n = 0; n < NH * 8; n += 8)
+                                if (f0 + n < c.d)
+                                    *reinterpret_cast<uint4*>(dst + f0 + n) =
+                                        make_uint4(ptx::pack_bf16x2(o[n][2 * h + e] * inv, o[n + 1][2 * h + e] * inv),
+                                                   ptx::pack_bf16x2(o[n + 2][2 * h + e] * inv, o[n + 3][2 * h + e] * inv),
+                                                   ptx::pack_bf16x2(o[n + 4][2 * h + e] * inv, o[n + 5][2 * h + e] * inv),
+                                                   ptx::pack_bf16x2(o[n + 6][2 * h + e] * inv, o[n + 7][2 * h + e] * inv));
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NH * 8; ++n)
+                            if (8 * n + 2 * t < c.d)
+                                *reinterpret_cast<uint32_t*>(dst + 8 * n + 2 * t) =
+                                    ptx::pack_bf16x2(o[n][2 * h] * inv, o[n][2 * h + 1] * inv);
+                    }
+                    if (t == 0 && p.lse) p.lse[row] = l[h] == 0.f ? -INFINITY : (m[h] + __log2f(l[h])) * 0.6931471805599453f;
+                }
+            } else {
+                // a part: the one that starts the unit goes to slot 2 cta + 1
+                const int ps = 2 * cta + (first == 0 ? 1 : 0);
+                float* po = p.part_o + ((long long)ps * C::MR + 16 * wr) * C::D;
+                float* pm = p.part_ml + ((long long)ps * C::MR + 16 * wr) * 2;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (tok[h] < 0) continue;
+                    const int r = g + 8 * h;
+#pragma unroll
+                    for (int n = 0; n < NH * 8; ++n) {
+                        if (Q8) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) po[r * C::D + out_col<true, NH>(n, e, t)] = o[n][2 * h + e];
+                        } else {
+                            *reinterpret_cast<float2*>(po + r * C::D + 8 * n + 2 * t) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
+                        }
+                    }
+                    if (t == 0) *reinterpret_cast<float2*>(pm + r * 2) = make_float2(m[h], l[h]);
+                }
+                if (first == 0 && warp == 0 && lane == 0) {
+                    // parts up to the one that holds the unit's last stage
+                    const long long last = hi - left + u.st - 1;  // its index in the list (this piece starts at hi - left)
+                    const int c_last = (int)(((last + 1) * W + total - 1) / total) - 1;
+                    p.desc[cta] = make_int4(b, kvh, rt, c_last - cta + 1);
+                }
+            }
+        }
+        left -= end - first;
+        if (left > 0) next_unit();
+    }
+}
+
+// Joins the parts of cut units, in their order: one warp per row. Block
+// (x, y): rows 4y .. 4y+3 of the unit whose first part CTA x of the attention
+// wrote.
+template <int MR, int D>
+__global__ void __launch_bounds__(128) paged_join_kernel(const DecParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 ds = p.desc[blockIdx.x];
+    const int parts = ds.w;
+    if (parts == 0) return;
+    const int lane = threadIdx.x % 32, r = blockIdx.y * 4 + threadIdx.x / 32;
+    const SeqInfo sq = seq_info(p.c, ds.x);
+    const int row = ds.z * MR + r;
+    if (row >= sq.n * p.G) return;
+    auto slot = [&](int i) { return i == 0 ? 2 * (long long)blockIdx.x + 1 : 2 * ((long long)blockIdx.x + i); };
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[(slot(i) * MR + r) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    constexpr int E = D / 32;
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot(i) * MR + r) * 2);
+        const float w = ptx::ex2(ml.x - ref);
+        const float* po = p.part_o + (slot(i) * MR + r) * D + lane * E;
+        l += ml.y * w;
+        if (E == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(po);
+            acc[0] += v.x * w; acc[1] += v.y * w; acc[E - 2] += v.z * w; acc[E - 1] += v.w * w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(po);
+            acc[0] += v.x * w; acc[1] += v.y * w;
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long orow = (long long)(sq.q0 + row / p.G) * p.Hq + ds.y * p.G + row % p.G;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        if (lane * E + e < p.c.d)
+            *reinterpret_cast<uint32_t*>(p.out + orow * p.c.d + lane * E + e) = ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+}
+
+constexpr int kParts = 2 * 148;  // two CTAs per SM
+
+int rows_class(int max_q, int G) {
+    const long long r = (long long)max_q * G;
+    return r <= 16 ? 1 : r <= 32 ? 2 : 4;
+}
+
+bool encode(CUtensorMap* m, bool u8, const void* base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+            const cuuint32_t (&box)[4]) {
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return false;
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(m, u8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool Q8, int NH, int WR>
+cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
+    using C = Cfg<Q8, NH, WR>;
+    DecParams p;
+    memset(&p, 0, sizeof(p));
+    const PagedCache& c = a.c;
+    const cuuint64_t d = c.d, P = c.page_size, e = Q8 ? 1 : 2;
+    {
+        const cuuint64_t dims[4] = {d, P, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_pages};
+        const cuuint64_t st[3] = {d * e, P * d * e, c.Hkv * P * d * e};
+        const cuuint32_t box[4] = {Q8 ? 128u : 64u, (cuuint32_t)kSliceRows, 1, 1};
+        if (!encode(&p.tm_k, Q8, a.k_pages, dims, st, box) || !encode(&p.tm_v, Q8, a.v_pages, dims, st, box))
+            return cudaErrorInvalidValue;
+    }
+    if (a.Ld > 0) {
+        // dimensions: feature, kv-head, slot (those in use), token
+        const cuuint64_t dims[4] = {d, (cuuint64_t)c.Hkv, (cuuint64_t)a.Ld, (cuuint64_t)c.N};
+        const cuuint64_t st[3] = {d * 2, c.Hkv * d * 2, (cuuint64_t)a.Ld_cap * c.Hkv * d * 2};
+        const cuuint32_t box[4] = {64, 1, (cuuint32_t)kSliceRows, 1};
+        if (!encode(&p.tm_kd, false, a.kd, dims, st, box) || !encode(&p.tm_vd, false, a.vd, dims, st, box))
+            return cudaErrorInvalidValue;
+    } else {
+        p.tm_kd = p.tm_k;
+        p.tm_vd = p.tm_v;
+    }
+    p.c = c;
+    p.q = static_cast<const __nv_bfloat16*>(a.q);
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.out = static_cast<__nv_bfloat16*>(a.out);
+    p.lse = a.lse;
+    p.Hq = a.Hq; p.G = a.G; p.Ld = a.Ld; p.DSL = (a.Ld + kSliceRows - 1) / kSliceRows;
+    p.W = kParts;
+    p.min_stages = 4;
+    p.sl2 = a.scale * 1.4426950408889634f;
+    p.status = a.status;
+    p.wait_limit = a.wait_limit;
+    char* ws = static_cast<char*>(a.workspace);
+    p.desc = reinterpret_cast<int4*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + kParts * sizeof(int4));
+    p.part_o = p.part_ml + (size_t)2 * kParts * C::MR * 2;
+    auto kern = paged_dec_kernel<Q8, NH, WR>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (err != cudaSuccess) return err;
+    kern<<<kParts, kThreads, C::kSmem, s>>>(p);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    // the join is launched while the attention drains and waits for its end
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(kParts, C::MR / 4);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::MR, C::D>, p);
+}
+
+template <bool Q8, int NH>
+cudaError_t by_rows(const PagedFwdArgs& a, cudaStream_t s) {
+    switch (rows_class(a.max_q, a.G)) {
+        case 1: return launch<Q8, NH, 1>(a, s);
+        case 2: return launch<Q8, NH, 2>(a, s);
+        default: return launch<Q8, NH, 4>(a, s);
+    }
+}
+
+}  // namespace
+
+bool paged_dec_supported(const PagedFwdArgs& a) {
+    const PagedCache& c = a.c;
+    if (a.dtype != MODA_BF16 || c.d % 8 || c.d > 128 || c.page_size % kSliceRows) return false;
+    if (a.k_scale && c.d % 16) return false;  // TMA strides are multiples of 16 bytes
+    return (long long)c.N * a.Hq < (1LL << 31);
+}
+
+size_t paged_dec_workspace(int max_q, int G, int d) {
+    const size_t mr = 16 * rows_class(max_q, G), D = d <= 64 ? 64 : 128;
+    return kParts * sizeof(int4) + 2 * (size_t)kParts * mr * (D + 2) * sizeof(float);
+}
+
+cudaError_t launch_paged_dec(const PagedFwdArgs& a, cudaStream_t s) {
+    if (a.k_scale) return a.c.d <= 64 ? by_rows<true, 1>(a, s) : by_rows<true, 2>(a, s);
+    return a.c.d <= 64 ? by_rows<false, 1>(a, s) : by_rows<false, 2>(a, s);
+}
+
+}  // namespace moda
