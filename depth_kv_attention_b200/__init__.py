@@ -476,7 +476,8 @@ def _append(where, fn, q, k, v, pages, scales, block_table, cu_q, ctx_lens, rope
 
 
 def _stream_addr(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    # the raw handle: making a Stream object costs as much as a launch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def moda_paged_append(q, k, v, k_pages, v_pages, block_table, cu_q, ctx_lens, rope=None, interleaved: bool = False,

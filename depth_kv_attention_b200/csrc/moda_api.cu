@@ -605,7 +605,10 @@ moda_status run_fwd_paged(const void* q, const void* k_pages, const void* v_page
     if (impl == MODA_IMPL_TC2 || (impl == MODA_IMPL_TC && !tc_ok)) return MODA_ERR_UNSUPPORTED;
     if (status_ptr(&a.status, &a.wait_limit) != cudaSuccess) return MODA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = tc_ok && impl != MODA_IMPL_SIMT ? launch_paged_dec(a, s) : launch_paged_fwd_simt(a, s);
+    cudaError_t e;
+    if (!tc_ok || impl == MODA_IMPL_SIMT) e = launch_paged_fwd_simt(a, s);
+    else if ((long long)max_q * a.G >= kPagedPreRows && paged_pre_supported(a)) e = launch_paged_pre(a, s);
+    else e = launch_paged_dec(a, s);
     return e == cudaSuccess ? MODA_OK : MODA_ERR_LAUNCH;
 }
 
@@ -636,7 +639,10 @@ moda_status moda_paged_append_q8(const void* q, const void* k, const void* v, lo
 
 size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d, moda_dtype dtype) {
     if (N < 1 || B < 1 || max_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1 || d > 128) return 0;
-    return dtype == MODA_BF16 ? paged_dec_workspace(max_q, Hq / Hkv, d) : 0;
+    if (dtype != MODA_BF16) return 0;
+    const size_t dec = paged_dec_workspace(max_q, Hq / Hkv, d);
+    const bool pre = (long long)max_q * (Hq / Hkv) >= kPagedPreRows && d == 128;
+    return pre && paged_pre_workspace() > dec ? paged_pre_workspace() : dec;
 }
 
 moda_status moda_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* kd, const void* vd,

@@ -38,6 +38,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "paged_join.cuh"
 #include "paged_units.cuh"
 #include "sm100_ptx.cuh"
 #include "tmap_host.h"
@@ -61,12 +62,16 @@ struct DecParams {
     float* lse;
     float* part_o;   // [2W][MR][D]
     float* part_ml;  // [2W][MR][2]
-    int4* desc;      // [W]: {sequence, kv-head, tile, parts}, parts = 0: none
+    int4* desc;      // [W]: {sequence, kv-head, tile, parts | rows << 16}, 0: no unit is cut there
     int Hq, G, Ld, DSL, W, min_stages;
+    int split;       // units may be cut (else each stays with one CTA)
     float sl2;
     unsigned int* status;
     unsigned int wait_limit;
 };
+
+constexpr int kSeqs = 128;   // sequences whose lengths are kept in shared memory
+constexpr int kCtl = 3072;   // barriers and those
 
 template <bool Q8, int NH, int WR>
 struct Cfg {
@@ -80,7 +85,7 @@ struct Cfg {
     static constexpr int DS = kSlot / kDepSlice;             // depth slices per stage
     static constexpr int NS = Q8 || NH == 1 ? 8 : 5;         // ring slots
     static constexpr int kMerge = WK == 1 ? 0 : 2 * 16 * D * 4;
-    static constexpr int kSmem = 1024 + NS * kSlot + kMerge + 1024;
+    static constexpr int kSmem = 1024 + NS * kSlot + kMerge + kCtl;
 };
 
 struct __align__(8) DecBars {
@@ -92,8 +97,9 @@ struct __align__(8) DecBars {
     long long total, before;
     int begin_seq;
     int abort_flag;
+    SeqInfo seqs[kSeqs];
 };
-static_assert(sizeof(DecBars) <= 1024, "barrier block");
+static_assert(sizeof(DecBars) <= kCtl, "barrier block");
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -288,6 +294,7 @@ __device__ __forceinline__ void add_nonfinite(uint32_t slice, uint32_t bad, cons
             const float a = (k & 8) ? ((k & 1) ? p[1][2 * h + 1] : p[1][2 * h]) : ((k & 1) ? p[0][2 * h + 1] : p[0][2 * h]);
             pr[h] = __shfl_sync(0xffffffffu, a, src);
         }
+        if (!__any_sync(0xffffffffu, pr[0] != 0.f || pr[1] != 0.f)) continue;  // what an unused row of a page held
 #pragma unroll
         for (int nt = 0; nt < NH * 8; ++nt)
 #pragma unroll
@@ -345,7 +352,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
     const int per = (c.B + kThreads - 1) / kThreads;
     const int b0 = min(threadIdx.x * per, c.B), b1 = min(b0 + per, c.B);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seq_stages<C::MR>(seq_info(c, b), p.G, p.DSL, C::DS, max_keys);
+    for (int b = b0; b < b1; ++b) {
+        const SeqInfo s = seq_info(c, b);
+        if (b < kSeqs) bars->seqs[b] = s;
+        mine += seq_stages<C::MR>(s, p.G, p.DSL, C::DS, max_keys);
+    }
+    auto seq_at = [&](int b) { return b < kSeqs ? bars->seqs[b] : seq_info(c, b); };
     long long incl = mine * c.Hkv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -369,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
         long long at = incl - mine * c.Hkv;
         if (lo >= at && lo < incl) {  // one thread: the CTA's part begins in its run
             for (int b = b0; b < b1; ++b) {
-                const long long n = seq_stages<C::MR>(seq_info(c, b), p.G, p.DSL, C::DS, max_keys) * c.Hkv;
+                const long long n = seq_stages<C::MR>(seq_at(b), p.G, p.DSL, C::DS, max_keys) * c.Hkv;
                 if (lo < at + n) {
                     bars->begin_seq = b;
                     bars->begin_in_seq = lo - at;
@@ -389,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
     // ---- the units of this part, walked alike by every warp
     int b = bars->begin_seq, kvh, rt = 0;
     long long left = hi - lo;       // stages still to do
-    SeqInfo sq = seq_info(c, b);
+    SeqInfo sq = seq_at(b);
     int first;                      // first stage of the current unit's piece
     {
         long long in = bars->begin_in_seq;
@@ -410,16 +422,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
         if (++kvh < c.Hkv) return;
         kvh = 0;
         do {
-            sq = seq_info(c, ++b);
+            sq = seq_at(++b);
         } while (sq.n == 0 && b + 1 < c.B);  // `left` > 0: a later sequence has stages
     };
+
+    if (!p.split && first > 0) {  // the unit belongs to the CTA it starts in
+        left -= unit_shape<C::MR>(sq, rt, p.G, p.DSL, C::DS, max_keys).st - first;
+        if (left > 0) next_unit();
+    }
 
     if (warp == kProducer) {
         int slot = 0, ph = 1, issued = 0;
         bool ok = true;
         while (left > 0) {
             const UnitShape u = unit_shape<C::MR>(sq, rt, p.G, p.DSL, C::DS, max_keys);
-            const int end = (int)min((long long)u.st, first + left);
+            const int end = p.split ? (int)min((long long)u.st, first + left) : u.st;
             // page slices [4 first, ...) of the unit, 32 at a time: lane l
             // holds slice 32 batch + l of the piece; the next batch's page ids
             // are in flight while this one's boxes are issued
@@ -513,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
     bool ok = true;
     while (left > 0) {
         const UnitShape u = unit_shape<C::MR>(sq, rt, p.G, p.DSL, C::DS, max_keys);
-        const int end = (int)min((long long)u.st, first + left);
+        const int end = p.split ? (int)min((long long)u.st, first + left) : u.st;
         // this lane's rows g and g + 8 of the warp's 16
         int tok[2], pos[2];
         uint32_t qf[NH * 4][4];
@@ -792,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
                     // parts up to the one that holds the unit's last stage
                     const long long last = hi - left + u.st - 1;  // its index in the list (this piece starts at hi - left)
                     const int c_last = (int)(((last + 1) * W + total - 1) / total) - 1;
-                    p.desc[cta] = make_int4(b, kvh, rt, c_last - cta + 1);
+                    p.desc[cta] = make_int4(b, kvh, rt, (c_last - cta + 1) | u.rows << 16);
                 }
             }
         }
@@ -801,54 +818,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
     }
 }
 
-// Joins the parts of cut units, in their order: one warp per row. Block
-// (x, y): rows 4y .. 4y+3 of the unit whose first part CTA x of the attention
-// wrote.
-template <int MR, int D>
-__global__ void __launch_bounds__(128) paged_join_kernel(const DecParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 ds = p.desc[blockIdx.x];
-    const int parts = ds.w;
-    if (parts == 0) return;
-    const int lane = threadIdx.x % 32, r = blockIdx.y * 4 + threadIdx.x / 32;
-    const SeqInfo sq = seq_info(p.c, ds.x);
-    const int row = ds.z * MR + r;
-    if (row >= sq.n * p.G) return;
-    auto slot = [&](int i) { return i == 0 ? 2 * (long long)blockIdx.x + 1 : 2 * ((long long)blockIdx.x + i); };
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[(slot(i) * MR + r) * 2]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    constexpr int E = D / 32;
-    float acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot(i) * MR + r) * 2);
-        const float w = ptx::ex2(ml.x - ref);
-        const float* po = p.part_o + (slot(i) * MR + r) * D + lane * E;
-        l += ml.y * w;
-        if (E == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(po);
-            acc[0] += v.x * w; acc[1] += v.y * w; acc[E - 2] += v.z * w; acc[E - 1] += v.w * w;
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(po);
-            acc[0] += v.x * w; acc[1] += v.y * w;
-        }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const long long orow = (long long)(sq.q0 + row / p.G) * p.Hq + ds.y * p.G + row % p.G;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-        if (lane * E + e < p.c.d)
-            *reinterpret_cast<uint32_t*>(p.out + orow * p.c.d + lane * E + e) = ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
-}
-
-constexpr int kParts = 2 * 148;  // two CTAs per SM
+constexpr int kParts = 2 * 148;   // two CTAs per SM
+constexpr int kWholeKeys = 512;
+constexpr int kMinStages = 1;
 
 int rows_class(int max_q, int G) {
     const long long r = (long long)max_q * G;
@@ -898,7 +870,10 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
     p.lse = a.lse;
     p.Hq = a.Hq; p.G = a.G; p.Ld = a.Ld; p.DSL = (a.Ld + kSliceRows - 1) / kSliceRows;
     p.W = kParts;
-    p.min_stages = 4;
+    p.min_stages = kMinStages;
+    // the longest unit the block table allows, in stages: short ones stay whole
+    // and save the join
+    p.split = (long long)c.max_blocks * c.page_size + (long long)a.Ld * ((C::MR + a.G - 2) / a.G + 1) > kWholeKeys;
     p.sl2 = a.scale * 1.4426950408889634f;
     p.status = a.status;
     p.wait_limit = a.wait_limit;
@@ -907,23 +882,14 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
     p.part_ml = reinterpret_cast<float*>(ws + kParts * sizeof(int4));
     p.part_o = p.part_ml + (size_t)2 * kParts * C::MR * 2;
     auto kern = paged_dec_kernel<Q8, NH, WR>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static SmemLimit limit;
+    cudaError_t err = limit.raise(reinterpret_cast<const void*>(kern), C::kSmem);
     if (err != cudaSuccess) return err;
     kern<<<kParts, kThreads, C::kSmem, s>>>(p);
     err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    // the join is launched while the attention drains and waits for its end
-    cudaLaunchConfig_t cfg;
-    memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(kParts, C::MR / 4);
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::MR, C::D>, p);
+    if (err != cudaSuccess || !p.split) return err;
+    JoinParams j{p.c, p.out, p.lse, p.part_o, p.part_ml, p.desc, p.Hq, p.G};
+    return launch_paged_join<C::MR, C::D, kParts>(j, s);
 }
 
 template <bool Q8, int NH>
