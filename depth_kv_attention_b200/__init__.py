@@ -80,7 +80,7 @@ _ll = ctypes.c_longlong
 _APPEND = [_vp] * 3 + [_ll] * 3 + [_vp, _i, _i, _i] + [_vp] * 3 + [_i] * 9
 _c_append = _sig("moda_paged_append", _i, _APPEND + [_vp] * 5 + [_i, _i, _vp])
 _c_append_q8 = _sig("moda_paged_append_q8", _i, _APPEND + [_vp] * 7 + [_i, _i, _vp])
-_c_paged_ws = _sig("moda_fwd_paged_workspace_bytes", _sz, [_i] * 7)
+_c_paged_ws = _sig("moda_fwd_paged_workspace_bytes", _sz, [_i] * 10)
 _PAGED = [_vp] * 5 + [_i] * 12 + [_f, _vp, _vp, _vp, _sz, _vp, _i]
 _c_fwd_paged = _sig("moda_fwd_paged", _i, [_vp] * 3 + _PAGED)
 _c_fwd_paged_q8 = _sig("moda_fwd_paged_q8", _i, [_vp] * 5 + _PAGED)
@@ -507,8 +507,8 @@ def _paged_ws(*dims):
     return _c_paged_ws(*dims)
 
 
-def moda_fwd_paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, dtype) -> int:
-    return _c_paged_ws(N, B, max_q, Hq, Hkv, d, _DTYPE[dtype])
+def moda_fwd_paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, num_pages, page_size, dtype, q8: bool = False) -> int:
+    return _c_paged_ws(N, B, max_q, Hq, Hkv, d, num_pages, page_size, _DTYPE[dtype], int(q8))
 
 
 def _fwd_paged(where, fn, q, pages, scales, block_table, cu_q, ctx_lens, max_q, kd, vd, Ld, scale, out, lse,
@@ -533,7 +533,7 @@ def _fwd_paged(where, fn, q, pages, scales, block_table, cu_q, ctx_lens, max_q, 
     if N == 0:
         return out, lse
     dt = _DTYPE[q.dtype]
-    need = _paged_ws(N, B, max_q, Hq, Hkv, d, dt)
+    need = _paged_ws(N, B, max_q, Hq, Hkv, d, num_pages, page_size, dt, scales is not None)
     with _on(q.device):
         if workspace is None and need:
             # from the pool of the stream it is used on

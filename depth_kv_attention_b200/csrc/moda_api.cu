@@ -595,7 +595,7 @@ moda_status run_fwd_paged(const void* q, const void* k_pages, const void* v_page
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned4(lse) ||
         !aligned4(k_scale) || !aligned4(v_scale) || (Ld > 0 && (!aligned16(kd) || !aligned16(vd))))
         return MODA_ERR_MISALIGNED;
-    const size_t need = moda_fwd_paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, dtype);
+    const size_t need = moda_fwd_paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, num_pages, page_size, dtype, k_scale != nullptr);
     if (need && (!workspace || workspace_bytes < need)) return MODA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MODA_ERR_MISALIGNED;
     a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.k_scale = k_scale; a.v_scale = v_scale;
@@ -637,12 +637,15 @@ moda_status moda_paged_append_q8(const void* q, const void* k, const void* v, lo
                       k_scale, v_scale, q_out, kd, vd, Ld, slot, stream);
 }
 
-size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d, moda_dtype dtype) {
-    if (N < 1 || B < 1 || max_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1 || d > 128) return 0;
-    if (dtype != MODA_BF16) return 0;
+size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d, int num_pages, int page_size,
+                                      moda_dtype dtype, int q8) {
+    if (N < 1 || B < 1 || max_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1 || d > 128 || num_pages < 1 || page_size < 1)
+        return 0;
+    if (dtype != MODA_BF16 || page_size % 16) return 0;
     const size_t dec = paged_dec_workspace(max_q, Hq / Hkv, d);
-    const bool pre = (long long)max_q * (Hq / Hkv) >= kPagedPreRows && d == 128;
-    return pre && paged_pre_workspace() > dec ? paged_pre_workspace() : dec;
+    if ((long long)max_q * (Hq / Hkv) < kPagedPreRows || d != 128) return dec;
+    const size_t pre = paged_pre_workspace(Hkv, num_pages, page_size, q8 != 0);
+    return pre > dec ? pre : dec;
 }
 
 moda_status moda_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* kd, const void* vd,

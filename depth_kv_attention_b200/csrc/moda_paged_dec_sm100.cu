@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
     // parts: at least min_stages stages each
     const int W = (int)max(1LL, min((long long)p.W, total / p.min_stages));
     if (cta >= W || total == 0) return;
-    const long long lo = total * cta / W, hi = total * (cta + 1) / W;
+    const long long lo = part_begin(total, cta, W), hi = part_begin(total, cta + 1, W);
     {
         long long at = incl - mine * c.Hkv;
         if (lo >= at && lo < incl) {  // one thread: the CTA's part begins in its run

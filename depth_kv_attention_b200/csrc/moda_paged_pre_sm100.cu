@@ -1,5 +1,6 @@
 // Attention over the paged sequence cache for many query rows per sequence
-// (chunks of prompts, wide drafts): bf16 or 8-bit pages, d = 128, on tcgen05.
+// (chunks of prompts, wide drafts): d = 128, on tcgen05. bf16 pages; 8-bit ones
+// are turned into bf16 once, ahead of it (see the end of the file).
 //
 // What it computes: as moda_paged_dec_sm100.cu, one softmax over the sequence
 // keys a new token sees and its own depth keys ("动态混合深度注意力机制MoDA技术解析",
@@ -17,14 +18,13 @@
 //    equal parts (paged_units.cuh): chunks are ragged and a few units rarely
 //    fill the GPU evenly. Roles run from piece to piece; a unit that is cut
 //    leaves (m, l, O) in the workspace for the join.
-//  * Conditioning warps see the tiles that cannot go to the tensor core as
-//    they came. 8-bit tiles become bf16 in place (a code times its page's
-//    power-of-two scale, exact). Value tiles in which some row is masked are
-//    cleared of non-finite elements (a masked P is 0, and 0 * NaN is not);
-//    rows that do see one get it added back when the piece ends.
+//  * Value tiles in which some row is masked pass through two conditioning
+//    warps, which clear their non-finite elements (a masked P is 0, and 0 * NaN
+//    is not); rows that do see one get it added back when the piece ends.
 //  * Every mbarrier wait is bounded, as in the dense forward.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -41,12 +41,11 @@ namespace {
 constexpr int kD = 128;
 constexpr int kTileBytes = 128 * kD * 2;
 constexpr int kHalfBytes = kTileBytes / 2;
-constexpr int kStages = 5;
 constexpr int kRows = 256;      // rows of a unit: two tiles
 constexpr int kItemKeys = 128;
 constexpr int kSlices = 8;      // 16-row slices of an item
 constexpr int kParts = 148;     // one CTA per SM
-constexpr int kMeta = 8;        // items whose slice notes are kept (the ring holds at most 3)
+constexpr int kMeta = 8;        // items whose slice notes are kept (the rings hold fewer than 5)
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr uint32_t kNoPollLimit = 0;
@@ -54,50 +53,47 @@ constexpr uint32_t kNoPollLimit = 0;
 struct PreParams {
     CUtensorMap tm_q, tm_k, tm_v, tm_kd, tm_vd;
     PagedCache c;
-    const float* k_scale;
-    const float* v_scale;
-    const __nv_bfloat16* v_pages;  // bf16 pages and depth values, read again only
-    const __nv_bfloat16* vd;       // for rows that see a non-finite value
+    const __nv_bfloat16* v_pages;  // values, read again only for rows that see
+    const __nv_bfloat16* vd;       // a non-finite one
     __nv_bfloat16* out;
     float* lse;
     float* part_o;
     float* part_ml;
     int4* desc;
-    int Hq, G, n, Ld, Ld_cap, DSL;
+    int Hq, G, n, lg_step, Ld, Ld_cap, DSL;  // a unit has 2n = 1 << lg_step tokens
+    int box_rows;  // rows of a page box: the largest power of two that divides the page size, at most 128
     float sl2;
     unsigned int* status;
     unsigned int wait_limit;
 };
 
-// Warpgroups 0, 1: softmax of tiles 0, 1. Warps 8, 9: producer, MMA. bf16:
-// warps 10-11 condition (16-bit tiles rarely need it); 8-bit: a fourth
-// warpgroup does, one key row per thread. Registers at launch and after
-// reallocation: 384 x 168 = 256 x 216 + 128 x 72; 512 x 128 = 256 x 200 + 256 x 56.
-template <bool Q8>
-struct Roles {
-    static constexpr int kThreads = Q8 ? 512 : 384;
-    static constexpr int kCondFirst = Q8 ? 12 : 10;
-    static constexpr int kCond = Q8 ? 128 : 64;  // conditioning threads
-    static constexpr int kSoftmaxRegs = Q8 ? 200 : 216;
-    static constexpr int kControlRegs = Q8 ? 56 : 72;
-};
+// Warpgroups 0, 1: softmax of tiles 0, 1. Warps 8, 9: producer, MMA; 10, 11
+// condition. Registers at launch and after reallocation:
+// 384 x 168 = 256 x 216 + 128 x 72.
+constexpr int kThreads = 384;
+constexpr int kCondFirst = 10;
+constexpr int kCond = 64;        // conditioning threads
+constexpr int kSoftmaxRegs = 216;
+constexpr int kControlRegs = 72;
+constexpr int kStages = 5;
 
 struct __align__(8) PreBars {
     uint64_t q_full, q_empty;
-    uint64_t full[kStages], empty[kStages], raw_full[kStages];
+    uint64_t full[kStages], empty[kStages];
+    uint64_t raw_full[kStages];      // a value tile that is to be conditioned has landed
     uint64_t s_full[2], p_full[2], o_final[2], o_empty[2];
     uint64_t drain;
-    float scale[kStages][kSlices];   // 8-bit: scale of each slice of a tile
     uint32_t holes[kMeta];           // per item: slices without a page
     int bad_piece[kMeta];            // last piece that met a non-finite value a row may see
     long long scan[16];
-    long long begin_in_seq;
-    int begin_seq;
+    long long total, hi;             // items in all, end of this CTA's part
+    int W;                           // parts
     uint32_t tmem_base;
     int abort_flag;
 };
-constexpr int kSmemBytes = 2 * kTileBytes + kStages * kTileBytes + 1024 + 1024;
-static_assert(sizeof(PreBars) <= 1024, "barrier block");
+constexpr int kCtl = 2048;
+constexpr int kWalks = 12;  // one per warp
+constexpr int kSmemBytes = (2 + kStages) * kTileBytes + kCtl + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
 __device__ __forceinline__ void flag_timeout(PreParams const& p, PreBars* bars) {
@@ -139,25 +135,48 @@ __device__ __forceinline__ Unit make_unit(const PreParams& p, const SeqInfo& s, 
     return u;
 }
 
-__device__ __forceinline__ long long seq_items(const PreParams& p, const SeqInfo& s, long long max_keys) {
-    long long t = 0;
-    for (int rt = 0; rt * 2 * p.n < s.n; ++rt) t += make_unit(p, s, rt, max_keys).n_items;
+// Items of the sequence's first `tiles` units. Unit rt sees
+// min(pos0 + 2n (rt + 1), pos0 + n_tokens) keys; where no unit is clipped by
+// position 0 or by the table, ceil(keys / 128) over the whole units is a sum
+// of floor(t / m) over consecutive t (2n is a power of two that divides 128 m
+// or is 256), so it needs no loop.
+__device__ __forceinline__ long long items_before(const PreParams& p, const SeqInfo& s, int tiles, long long max_keys) {
+    const int step = 1 << p.lg_step;  // 2n
+    const long long last = (long long)s.pos0 + s.n;
+    if (s.pos0 < 0 || last > max_keys || step > kItemKeys) {
+        long long t = 0;
+        for (int rt = 0; rt < tiles; ++rt) t += make_unit(p, s, rt, max_keys).n_items;
+        return t;
+    }
+    const int whole = min(tiles, s.n >> p.lg_step);
+    const int lg_m = 7 - p.lg_step, m = 1 << lg_m;
+    const int q = (int)(((long long)s.pos0 + step + kItemKeys - 1) >> p.lg_step);  // ceil(K / 128) = floor((q + rt) / m)
+    auto f = [&](int x) {                                        // sum of floor(t / m), t < x
+        const long long k = x >> lg_m;
+        return ((k * (k - 1) / 2) << lg_m) + k * (x & (m - 1));
+    };
+    long long t = f(q + whole) - f(q) + (long long)whole * ((step * p.DSL + kSlices - 1) / kSlices);
+    if (tiles > whole) t += make_unit(p, s, whole, max_keys).n_items;
     return t;
 }
+__device__ __forceinline__ long long seq_items(const PreParams& p, const SeqInfo& s, long long max_keys) {
+    return items_before(p, s, (s.n + 2 * p.n - 1) >> p.lg_step, max_keys);
+}
+__device__ __forceinline__ long long table_keys(const PagedCache& c) {
+    return min((long long)c.max_blocks * c.page_size, 0x7fffff00LL);
+}
 
-// The pieces of this CTA's part, walked alike by every role.
+// The pieces of this CTA's part. Every warp walks them alike, with its own
+// state in shared memory: the loops keep in registers only what they use.
 struct Walk {
-    const PreParams& p;
-    long long max_keys, left;
-    int b, kvh, rt, first, piece;
+    int b, kvh, rt, first, piece, end, left;
     SeqInfo sq;
     Unit u;
-    int end;
-    __device__ __forceinline__ void shape() {
-        u = make_unit(p, sq, rt, max_keys);
-        end = (int)min((long long)u.n_items, first + left);
+    __device__ __forceinline__ void shape(const PreParams& p) {
+        u = make_unit(p, sq, rt, table_keys(p.c));
+        end = min(u.n_items, first + left);
     }
-    __device__ __forceinline__ bool next() {  // false: the part is done
+    __device__ __forceinline__ bool next(const PreParams& p) {  // false: the part is done
         left -= end - first;
         if (left <= 0) return false;
         first = 0;
@@ -171,65 +190,51 @@ struct Walk {
                 } while (sq.n == 0 && b + 1 < p.c.B);
             }
         }
-        shape();
+        shape(p);
         return true;
     }
 };
 
-// Two codes in bytes 0 and 2 of w, times the power of two in both halves of
-// sc2, as a bf16 pair (exact): (0x4300 | low 7 bits) is 128 + them,
-// (0x4300 | sign bit) is 128 or 256.
-__device__ __forceinline__ uint32_t scaled_codes(uint32_t w, __nv_bfloat162 sc2) {
-    const uint32_t y = (w & 0x007f007fu) | 0x43004300u, base = (w & 0x00800080u) | 0x43004300u;
-    __nv_bfloat162 a, b;
-    memcpy(&a, &y, 4);
-    memcpy(&b, &base, 4);
-    const __nv_bfloat162 r = __hmul2(__hsub2(a, b), sc2);
-    uint32_t o;
-    memcpy(&o, &r, 4);
-    return o;
-}
+static_assert(sizeof(PreBars) + kWalks * sizeof(Walk) <= kCtl && sizeof(PreBars) % 8 == 0, "control block");
 
-// Row r of a tile of 128 x 128 codes (plain 128-byte lines in the slot's
-// second half) to bf16 in the swizzled K-major layout of the whole slot. The
-// thread reads its row before it writes, and only its own line lies where it
-// writes features 64-127. Chunks are taken in an order that starts at the
-// row's number, so that neighbouring rows hit different banks.
-__device__ __forceinline__ void dequant_row(uint8_t* slot, int r, float scale) {
-    uint4 in[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        in[j] = *reinterpret_cast<const uint4*>(slot + kHalfBytes + r * 128 + (((j + r) & 7) << 4));
-    const __nv_bfloat162 sc2 = __float2bfloat162_rn(scale);
-#pragma unroll
-    for (int jj = 0; jj < 8; ++jj) {
-        const int j = (jj + r) & 7;  // codes 16 j .. 16 j + 15
-        const uint32_t w[4] = {in[jj].x, in[jj].y, in[jj].z, in[jj].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t lo = scaled_codes(w[q], sc2), hi = scaled_codes(w[q] >> 8, sc2);  // (0, 2), (1, 3)
-            o[2 * q] = __byte_perm(lo, hi, 0x5410);
-            o[2 * q + 1] = __byte_perm(lo, hi, 0x7632);
-        }
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const int oc = 2 * j + v;  // output chunk of 8 features
-            *reinterpret_cast<uint4*>(slot + (oc >> 3) * kHalfBytes + r * 128 + (((oc & 7) ^ (r & 7)) << 4)) =
-                make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-        }
+// A warp's step to its next piece: lane 0 walks, everyone sees the result.
+__device__ __forceinline__ bool next_piece(Walk* w, const PreParams& p, int lane) {
+    __syncwarp();
+    bool more = false;
+    if (lane == 0) {
+        Walk v = *w;
+        more = v.next(p);
+        *w = v;
     }
+    more = __shfl_sync(0xffffffffu, more, 0);
+    __syncwarp();
+    return more;
 }
 
 // Sets the non-finite elements of a bf16 value tile to 0. Returns whether this
-// thread met one in a row below `rows` (rows past it nobody sees).
-template <int THREADS>
+// thread met one in a row below `rows` (rows past it nobody sees). The usual
+// tile has none: 0 * x summed over everything is NaN exactly when one is there.
 __device__ __forceinline__ bool clear_nonfinite(uint8_t* slot, int ct, int rows) {
+    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+    __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
+#pragma unroll 8
+    for (int ch = ct; ch < kTileBytes / 16; ch += kCond) {
+        const uint4 v = *reinterpret_cast<const uint4*>(slot + ch * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            __nv_bfloat162 x;
+            memcpy(&x, &w[e], 4);
+            acc[e] = __hfma2(x, zero, acc[e]);
+        }
+    }
+    const __nv_bfloat162 sum = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+    const float2 f = __bfloat1622float2(sum);
+    if (f.x == 0.f && f.y == 0.f) return false;
     bool met = false;
-#pragma unroll 4
-    for (int ch = ct; ch < kTileBytes / 16; ch += THREADS) {
+    for (int ch = ct; ch < kTileBytes / 16; ch += kCond) {
         uint4* at = reinterpret_cast<uint4*>(slot + ch * 16);
-        uint4 v = *at;
+        const uint4 v = *at;
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
         bool any = false;
 #pragma unroll
@@ -245,13 +250,7 @@ __device__ __forceinline__ bool clear_nonfinite(uint8_t* slot, int ct, int rows)
     return met;
 }
 
-__device__ __forceinline__ void load_box(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1, int c2, int c3) {
-    ptx::tma_load_4d(dst, m, bar, c0, c1, c2, c3);
-}
-
-template <bool Q8>
-__global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const __grid_constant__ PreParams p) {
-    using R = Roles<Q8>;
+__global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_constant__ PreParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
@@ -286,13 +285,13 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
         p.desc[cta] = make_int4(0, 0, 0, 0);
     }
     // ---- the list of items: each thread sums a run of sequences, then a scan
-    Walk w{p};
-    w.max_keys = min((long long)c.max_blocks * c.page_size, 0x7fffff00LL);
+    Walk* walks = reinterpret_cast<Walk*>(bars + 1);
     {
-        const int per = (c.B + R::kThreads - 1) / R::kThreads;
+        const long long max_keys = table_keys(c);
+        const int per = (c.B + kThreads - 1) / kThreads;
         const int b0 = min((int)threadIdx.x * per, c.B), b1 = min(b0 + per, c.B);
         long long mine = 0;
-        for (int b = b0; b < b1; ++b) mine += seq_items(p, seq_info(c, b), w.max_keys);
+        for (int b = b0; b < b1; ++b) mine += seq_items(p, seq_info(c, b), max_keys);
         long long incl = mine * c.Hkv;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -300,28 +299,6 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
             if (lane >= o) incl += v;
         }
         if (lane == 31) bars->scan[warp] = incl;
-        __syncthreads();
-        long long total = 0, pre = 0;
-        for (int x = 0; x < R::kThreads / 32; ++x) {
-            if (x < warp) pre += bars->scan[x];
-            total += bars->scan[x];
-        }
-        incl += pre;
-        const int W = (int)max(1LL, min((long long)kParts, total));
-        if (cta >= W || total == 0) return;
-        const long long lo = total * cta / W, hi = total * (cta + 1) / W;
-        long long at = incl - mine * c.Hkv;
-        if (lo >= at && lo < incl) {
-            for (int b = b0; b < b1; ++b) {
-                const long long k = seq_items(p, seq_info(c, b), w.max_keys) * c.Hkv;
-                if (lo < at + k) {
-                    bars->begin_seq = b;
-                    bars->begin_in_seq = lo - at;
-                    break;
-                }
-                at += k;
-            }
-        }
         if (warp == 0) {
             ptx::tmem_alloc(&bars->tmem_base, 512);
             ptx::tmem_relinquish();
@@ -329,41 +306,53 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
         ptx::tc_fence_before();
         __syncthreads();
         ptx::tc_fence_after();
-        w.b = bars->begin_seq;
-        w.sq = seq_info(c, w.b);
-        long long in = bars->begin_in_seq;
-        const long long k = max(seq_items(p, w.sq, w.max_keys), 1LL);
-        w.kvh = (int)(in / k);
-        in -= w.kvh * k;
-        w.rt = 0;
-        for (;; ++w.rt) {
-            const int items = make_unit(p, w.sq, w.rt, w.max_keys).n_items;
-            if (in < items) break;
-            in -= items;
+        long long total = 0, pre = 0;
+        for (int x = 0; x < kThreads / 32; ++x) {
+            if (x < warp) pre += bars->scan[x];
+            total += bars->scan[x];
         }
-        w.first = (int)in;
-        w.left = hi - lo;
-        w.piece = 0;
-        w.shape();
-        // the first part of a cut unit says where its parts are
-        if (threadIdx.x == 0) {
-            Walk v = w;
-            long long at2 = lo;
-            for (;;) {
-                if (v.first == 0 && v.end < v.u.n_items) {
-                    const long long last = at2 + v.u.n_items - 1;
-                    const int c_last = (int)(((last + 1) * W + total - 1) / total) - 1;
-                    p.desc[cta] = make_int4(v.b, v.kvh, v.rt, (c_last - cta + 1) | min(v.u.ntok * p.G, kRows) << 16);
+        incl += pre;
+        const int W = (int)max(1LL, min((long long)kParts, total));
+        if (cta >= W || total == 0) {
+            if (warp == 0) ptx::tmem_dealloc(bars->tmem_base, 512);
+            return;
+        }
+        const long long lo = part_begin(total, cta, W), hi = part_begin(total, cta + 1, W);
+        long long at = incl - mine * c.Hkv;
+        if (lo >= at && lo < incl) {  // one thread: the part begins in its run
+            Walk w;
+            for (w.b = b0; w.b < b1; ++w.b) {
+                w.sq = seq_info(c, w.b);
+                const long long k = seq_items(p, w.sq, max_keys);
+                if (lo < at + k * c.Hkv) {
+                    long long in = lo - at;
+                    w.kvh = (int)(in / k);
+                    in -= w.kvh * k;
+                    int x = 0, y = ((w.sq.n + 2 * p.n - 1) >> p.lg_step) - 1;  // last unit that starts at or before `in`
+                    while (x < y) {
+                        const int mid = (x + y + 1) / 2;
+                        if (items_before(p, w.sq, mid, max_keys) <= in) x = mid; else y = mid - 1;
+                    }
+                    w.rt = x;
+                    w.first = (int)(in - items_before(p, w.sq, x, max_keys));
+                    break;
                 }
-                at2 += v.end - v.first;
-                if (!v.next()) break;
+                at += k * c.Hkv;
             }
+            w.left = (int)(hi - lo);
+            w.piece = 0;
+            w.shape(p);
+            for (int i = 0; i < kWalks; ++i) walks[i] = w;
+            bars->total = total;
+            bars->hi = hi;
+            bars->W = W;
         }
+        __syncthreads();
     }
     const uint32_t tmem = bars->tmem_base;
     const int n = p.n;
 
-    if (warp >= 8) ptx::setmaxnreg_dec<R::kControlRegs>();
+    if (warp >= 8) ptx::setmaxnreg_dec<kControlRegs>();
     if (warp == kProducerWarp) {
         // -------------------------------------------------------- TMA warp
         int st = 0;
@@ -380,35 +369,27 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
                 ptx::prefetch_tmap(&p.tm_vd);
             }
         }
-        for (bool more = true; more && ok; more = w.next()) {
-            const Unit& u = w.u;
-            const int sl0 = w.first * kSlices;
+        Walk* w = walks + 8;
+        for (bool more = true; more && ok; more = next_piece(w, p, lane)) {
+            const int first = w->first, end = w->end, piece = w->piece, kvh = w->kvh, b = w->b;
+            const int n_seq = w->u.n_seq, nk = w->u.nk, ntok = w->u.ntok;
+            const int row0 = w->sq.q0 + w->u.tok0, pos_first = w->sq.pos0 + w->u.tok0;
+            const int sl0 = first * kSlices;
             auto fetch = [&](int sl) {
                 int pg = -1;
-                if (sl < u.n_seq * kSlices && sl * 16 < u.nk) pg = page_of(c, w.b, sl * 16 / c.page_size);
+                if (sl < n_seq * kSlices && sl * 16 < nk) pg = page_of(c, b, sl * 16 / c.page_size);
                 return pg;
             };
-            auto scales = [&](int pg, float& a, float& e) {
-                a = e = 1.f;
-                if (Q8 && pg >= 0) {
-                    a = __ldg(p.k_scale + (long long)pg * c.Hkv + w.kvh);
-                    e = __ldg(p.v_scale + (long long)pg * c.Hkv + w.kvh);
-                }
-            };
             int page = fetch(sl0 + lane), page_next = fetch(sl0 + 32 + lane);
-            float ks, vs, ks_next = 1.f, vs_next = 1.f;
-            scales(page, ks, vs);
-            const int pos_first = w.sq.pos0 + u.tok0;
-            for (int x = w.first; x < w.end && ok; ++x, ++item) {
-                const bool seq = x < u.n_seq;
+            for (int x = first; x < end && ok; ++x, ++item) {
+                const bool seq = x < n_seq;
                 const int rel = x * kSlices - sl0;
                 if (seq && rel && (rel & 31) == 0) {
                     page = page_next;
-                    ks = ks_next;
-                    vs = vs_next;
                     page_next = fetch(sl0 + rel + 32 + lane);
                 }
-                if (seq && (rel & 31) == 16) scales(page_next, ks_next, vs_next);
+                const uint32_t none =
+                    __ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, page, (rel & 31) + (lane & 7)) < 0) & 0xffu;
                 for (int kv = 0; kv < 2; ++kv) {
                     if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bars->empty[st], ph, wait_limit, abort_flag))) {
                         if (lane == 0) flag_timeout(p, bars);
@@ -416,54 +397,43 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
                         break;
                     }
                     uint8_t* dst = sRing + st * kTileBytes;
-                    const bool raw = seq ? (Q8 || (kv && (x + 1) * kItemKeys - 1 > pos_first)) : kv;
+                    const bool raw = kv && (!seq || (x + 1) * kItemKeys - 1 > pos_first);
                     uint64_t* bar = raw ? &bars->raw_full[st] : &bars->full[st];
                     const uint32_t bit = 1u << st;
                     if (raw) raw_par ^= bit;
                     full_par ^= bit;
                     last_raw = raw ? last_raw | bit : last_raw & ~bit;
                     used |= bit;
+                    if (kv == 0 && lane == 0) bars->holes[item % kMeta] = seq ? none : 0;
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, kTileBytes);
+                    __syncwarp();
                     if (seq) {
-                        const int sl = lane & 7, half = (lane >> 3) & 1;
-                        const int src = (rel & 31) + sl;
-                        const int pg = __shfl_sync(0xffffffffu, page, src);
-                        const float sc = __shfl_sync(0xffffffffu, kv ? vs : ks, src);
-                        const uint32_t none = __ballot_sync(0xffffffffu, lane < 8 && pg < 0);
-                        if (Q8 && lane < 8) bars->scale[st][sl] = pg < 0 ? 0.f : sc;
-                        if (!kv && lane == 0) bars->holes[item % kMeta] = none;
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, Q8 ? kHalfBytes : kTileBytes);
-                        __syncwarp();
-                        const int row = pg < 0 ? 0 : (x * kSlices + sl) * 16 % c.page_size;
-                        const int pgc = pg < 0 ? c.num_pages : pg;  // outside the map: zeros
-                        if (Q8) {
-                            if (lane < 8)
-                                load_box(dst + kHalfBytes + sl * 2048, kv ? &p.tm_v : &p.tm_k, bar, 0, row, w.kvh, pgc);
-                        } else if (lane < 16) {
-                            load_box(dst + half * kHalfBytes + sl * 2048, kv ? &p.tm_v : &p.tm_k, bar, half * 64, row,
-                                     w.kvh, pgc);
-                        }
+                        // boxes of box_rows rows and half of the features
+                        const int half = lane & 1, r0 = (lane >> 1) * p.box_rows;
+                        const int pg = __shfl_sync(0xffffffffu, page, ((rel & 31) + (r0 >> 4)) & 31);
+                        if (r0 < kItemKeys)
+                            // a page that is not there lies outside the map: zeros
+                            ptx::tma_load_4d(dst + half * kHalfBytes + r0 * 128, kv ? &p.tm_v : &p.tm_k, bar, half * 64,
+                                             pg < 0 ? 0 : (x * kItemKeys + r0) % c.page_size, kvh,
+                                             pg < 0 ? c.num_pages : pg);
                     } else {
                         const int sl = lane & 7, half = (lane >> 3) & 1;
-                        const int y = (x - u.n_seq) * kSlices + sl;
+                        const int y = (x - n_seq) * kSlices + sl;
                         const int tok = p.DSL ? y / p.DSL : 0, s16 = p.DSL ? y % p.DSL : 0;
-                        if (!kv && lane == 0) bars->holes[item % kMeta] = 0;
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, kTileBytes);
-                        __syncwarp();
                         if (lane < 16)
-                            load_box(dst + half * kHalfBytes + sl * 2048, kv ? &p.tm_vd : &p.tm_kd, bar, half * 64, w.kvh,
-                                     s16 * 16, p.DSL && tok < u.ntok ? w.sq.q0 + u.tok0 + tok : c.N);
+                            ptx::tma_load_4d(dst + half * kHalfBytes + sl * 2048, kv ? &p.tm_vd : &p.tm_kd, bar,
+                                             half * 64, kvh, s16 * 16, p.DSL && tok < ntok ? row0 + tok : c.N);
                     }
                     if (++st == kStages) {
                         st = 0;
                         ph ^= 1;
                     }
                 }
-                if (x == w.first && ok) {
+                if (x == first && ok) {
                     // this piece's queries, once the piece before has used its own
-                    if (w.piece > 0) {
-                        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bars->q_empty, (w.piece - 1) & 1, wait_limit, abort_flag))) {
+                    if (piece > 0) {
+                        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bars->q_empty, (piece - 1) & 1, wait_limit, abort_flag))) {
                             if (lane == 0) flag_timeout(p, bars);
                             ok = false;
                             break;
@@ -472,9 +442,9 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
                     if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->q_full, 2 * kTileBytes);
                     __syncwarp();
                     if (lane < 4)
-                        load_box(sQ + (lane >> 1) * kTileBytes + (lane & 1) * kHalfBytes, &p.tm_q, &bars->q_full,
-                                 (lane & 1) * 64, w.kvh * p.G, w.sq.q0 + u.tok0 + (lane >> 1) * n, 0);
-                    q_par = w.piece + 1;  // query loads issued
+                        ptx::tma_load_4d(sQ + (lane >> 1) * kTileBytes + (lane & 1) * kHalfBytes, &p.tm_q, &bars->q_full,
+                                 (lane & 1) * 64, kvh * p.G, row0 + (lane >> 1) * n, 0);
+                    q_par = piece + 1;  // query loads issued
                 }
             }
         }
@@ -521,23 +491,39 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
                 }
             };
             bool ok = true;
-            for (bool more = true; more && ok; more = w.next()) {
-                const Unit& u = w.u;
-                ok = wait_all(&bars->q_full, w.piece & 1);
+            Walk* w = walks + 9;
+            for (bool more = true; more && ok; more = w->next(p)) {
+                const Unit u = w->u;
+                const int first = w->first, end = w->end, piece = w->piece;
+                ok = wait_all(&bars->q_full, piece & 1);
                 if (!ok) break;
                 ok = wait_all(&bars->full[st], ph);
                 if (!ok) break;
-                if (u.part(0, w.first)) issue_s(0, st);
-                if (u.part(1, w.first)) issue_s(1, st);
+                if (u.part(0, first)) issue_s(0, st);
+                if (u.part(1, first)) issue_s(1, st);
                 ptx::mma_commit(&bars->empty[st]);
                 advance();
                 int cnt0 = 0, cnt1 = 0;      // items of this piece each tile has taken part in
-                for (int x = w.first; x < w.end && ok; ++x) {
+                // the last one of each (first - 1: none): its O is final there
+                const int last0 = min(end, u.dhi0) > max(first, u.n_seq) ? min(end, u.dhi0) - 1
+                                                                         : max(min(end, u.nkv0), first) - 1;
+                const int last1 = min(end, u.dhi1) > max(first, u.dlo1) ? min(end, u.dhi1) - 1
+                                                                        : max(min(end, u.nkv1), first) - 1;
+                // o_final may run at most one piece ahead of either tile's warps,
+                // also of a tile that takes no part in these pieces
+                auto finish = [&](int i) {
+                    if (piece > 0 && !wait_all(&bars->o_empty[i], (piece - 1) & 1)) return false;
+                    ptx::mma_commit(&bars->o_final[i]);
+                    return true;
+                };
+                if (last0 < first) ok = finish(0);
+                if (ok && last1 < first) ok = finish(1);
+                for (int x = first; x < end && ok; ++x) {
                     const int st_v = st;
                     ok = wait_all(&bars->full[st], ph);
                     if (!ok) break;
                     advance();
-                    const bool next = x + 1 < w.end;
+                    const bool next = x + 1 < end;
                     const uint64_t vd = v0 + (uint64_t)st_v * kSlotUnits;
                     bool k_ready = false;
 #pragma unroll
@@ -557,6 +543,10 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
                                 ptx::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, vd + (uint64_t)(k * 128), idesc_pv,
                                             (cnt > 0 || k > 0) ? 1u : 0u);
                             if (i) ++cnt1; else ++cnt0;
+                            if (x == (i ? last1 : last0) && !finish(i)) {
+                                ok = false;
+                                break;
+                            }
                         }
                         if (next && u.part(i, x + 1)) {
                             if (!k_ready) {
@@ -576,58 +566,48 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
                         advance();
                     }
                 }
-                // o_final may run at most one piece ahead of either tile's warps,
-                // also of a tile that takes no part in these pieces
-                if (ok && w.piece > 0)
-                    ok = wait_all(&bars->o_empty[0], (w.piece - 1) & 1) && wait_all(&bars->o_empty[1], (w.piece - 1) & 1);
-                if (ok) {
-                    ptx::mma_commit(&bars->q_empty);
-                    ptx::mma_commit(&bars->o_final[0]);
-                    ptx::mma_commit(&bars->o_final[1]);
-                }
+                if (ok) ptx::mma_commit(&bars->q_empty);
             }
             ptx::mma_commit(&bars->drain);
             ptx::mbar_wait(&bars->drain, 0, kNoPollLimit, nullptr);
         }
         __syncwarp();
-    } else if (warp >= R::kCondFirst) {
+    } else if (warp >= kCondFirst) {
         // ---------------------------------------------------- conditioning
-        const int ct = threadIdx.x - R::kCondFirst * 32;
+        const int ct = threadIdx.x - kCondFirst * 32;
         int st = 0;
         uint32_t raw_par = 0;
         bool ok = true;
-        for (bool more = true; more && ok; more = w.next()) {
-            const Unit& u = w.u;
-            const int pos_first = w.sq.pos0 + u.tok0;
-            for (int x = w.first; x < w.end && ok; ++x)
-                for (int kv = 0; kv < 2; ++kv) {
-                    const bool seq = x < u.n_seq;
-                    const bool raw = seq ? (Q8 || (kv && (x + 1) * kItemKeys - 1 > pos_first)) : kv;
-                    const int s = st;
+        Walk* w = walks + warp;
+        for (bool more = true; more && ok; more = next_piece(w, p, lane)) {
+            const int end = w->end, piece = w->piece, n_seq = w->u.n_seq, nk = w->u.nk;
+            const int pos_first = w->sq.pos0 + w->u.tok0;
+            for (int x = w->first; x < end && ok; ++x) {
+                const bool seq = x < n_seq;
+                for (int kv = 0; kv < 2 && ok; ++kv) {
+                    uint8_t* slot = sRing + st * kTileBytes;
+                    uint64_t* full = &bars->full[st];
+                    if (kv && (!seq || (x + 1) * kItemKeys - 1 > pos_first)) {
+                        const bool got = ptx::mbar_wait(&bars->raw_full[st], (raw_par >> st) & 1, wait_limit, abort_flag);
+                        raw_par ^= 1u << st;
+                        if (!ptx::bar_and(1, kCond, got)) {
+                            if (ct == 0) flag_timeout(p, bars);
+                            ok = false;
+                            break;
+                        }
+                        const int rows = seq ? min(nk - x * kItemKeys, kItemKeys) : kItemKeys;
+                        if (clear_nonfinite(slot, ct, rows)) bars->bad_piece[piece % kMeta] = piece;
+                        ptx::fence_proxy_async_smem();
+                        ptx::bar_sync(1, kCond);
+                        if (ct == 0) ptx::mbar_arrive(full);
+                    }
                     if (++st == kStages) st = 0;
-                    if (!raw) continue;
-                    const bool got = ptx::mbar_wait(&bars->raw_full[s], (raw_par >> s) & 1, wait_limit, abort_flag);
-                    raw_par ^= 1u << s;
-                    if (!ptx::bar_and(1, R::kCond, got)) {
-                        if (ct == 0) flag_timeout(p, bars);
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* slot = sRing + s * kTileBytes;
-                    if (Q8 && seq) {
-                        dequant_row(slot, ct, bars->scale[s][ct >> 4]);
-                    } else {
-                        const int rows = seq ? min(u.nk - x * kItemKeys, kItemKeys) : kItemKeys;
-                        if (clear_nonfinite<R::kCond>(slot, ct, rows)) bars->bad_piece[w.piece % kMeta] = w.piece;
-                    }
-                    ptx::fence_proxy_async_smem();  // generic writes before the tensor core's reads
-                    ptx::bar_sync(1, R::kCond);
-                    if (ct == 0) ptx::mbar_arrive(&bars->full[s]);
                 }
+            }
         }
     } else if (warp < 8) {
         // ---------------------------------------------- softmax warpgroups
-        ptx::setmaxnreg_inc<R::kSoftmaxRegs>();
+        ptx::setmaxnreg_inc<kSoftmaxRegs>();
         const int i = warp / 4;
         const int r = (warp % 4) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp % 4) * 32) << 16;
@@ -637,13 +617,16 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
         bool ok = true;
         uint32_t sp = 0;                      // s_full phase
         int item = 0;
-        for (bool more = true; more && ok; more = w.next()) {
-            const Unit& u = w.u;
-            const int pos = w.sq.pos0 + u.tok0 + tl;
+        Walk* w = walks + warp;
+        for (bool more = true; more && ok; more = next_piece(w, p, lane)) {
+            const int first = w->first, end = w->end, piece = w->piece, n_seq = w->u.n_seq;
+            const int pos = w->sq.pos0 + w->u.tok0 + tl;
             float m = -INFINITY, l = 0.f;
             int it = 0;
-            for (int x = w.first; x < w.end; ++x, ++item) {
-                if (!u.part(i, x)) continue;
+            // this tile's items: sequence items below nkv, depth items [dlo, dhi)
+            const int nkv = i ? w->u.nkv1 : w->u.nkv0, dlo = i ? w->u.dlo1 : n_seq, dhi = i ? w->u.dhi1 : w->u.dhi0;
+            for (int x = first; x < end; ++x, ++item) {
+                if (!(x < nkv || (x >= dlo && x < dhi))) continue;
                 const bool got = ptx::mbar_wait(&bars->s_full[i], sp, wait_limit, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) {
                     if (lane == 0) flag_timeout(p, bars);
@@ -652,7 +635,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
                 }
                 sp ^= 1;
                 ptx::tc_fence_after();
-                const bool seq = x < u.n_seq;
+                const bool seq = x < n_seq;
                 const int kbase = x * kItemKeys;
                 const uint32_t holes = bars->holes[item % kMeta];
                 softmax_columns(
@@ -671,7 +654,7 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
                             }
                         } else {
                             uint32_t vis[4];
-                            depth_col_mask((tl * p.DSL - (x - u.n_seq) * kSlices) * 16, p.Ld, false, 0ull, vis);
+                            depth_col_mask((tl * p.DSL - (x - n_seq) * kSlices) * 16, p.Ld, false, 0ull, vis);
 #pragma unroll
                             for (int k = 0; k < 128; ++k)
                                 if (!((vis[k >> 5] >> (k & 31)) & 1u)) s[k] = -INFINITY;
@@ -683,19 +666,20 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
                 ++it;
             }
             if (!ok) break;
-            const bool got = ptx::mbar_wait(&bars->o_final[i], w.piece & 1, wait_limit, abort_flag);
+            const bool got = ptx::mbar_wait(&bars->o_final[i], piece & 1, wait_limit, abort_flag);
             if (!__all_sync(0xffffffffu, got)) {
                 if (lane == 0) flag_timeout(p, bars);
                 ok = false;
                 break;
             }
             ptx::tc_fence_after();
-            const bool valid = tl < u.ntok;
-            const bool whole = w.first == 0 && w.end == u.n_items;
-            const int ps = 2 * cta + (w.first == 0 ? 1 : 0);
+            const int kvh = w->kvh;
+            const bool valid = tl < w->u.ntok;
+            const bool whole = first == 0 && end == w->u.n_items;
+            const int ps = 2 * cta + (first == 0 ? 1 : 0);
             const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-            const long long row = (long long)(w.sq.q0 + u.tok0 + tl) * p.Hq + w.kvh * p.G + hh;
-            const bool bad = *reinterpret_cast<volatile int*>(&bars->bad_piece[w.piece % kMeta]) == w.piece;
+            const long long row = (long long)(w->sq.q0 + w->u.tok0 + tl) * p.Hq + kvh * p.G + hh;
+            const bool bad = *reinterpret_cast<volatile int*>(&bars->bad_piece[piece % kMeta]) == piece;
 #pragma unroll 1
             for (int cc = 0; cc < 4; ++cc) {
                 uint32_t o[32];
@@ -715,19 +699,19 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
                             if (!(fabsf(f) <= 3.4e38f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
                         }
                     };
-                    if (!Q8) {
-                        const int pf = w.sq.pos0 + u.tok0;  // tiles that end past it were cleared
-                        const int x0 = max(w.first, max(0, pf + 1) / kItemKeys), x1 = min(w.end, u.n_seq);
-                        for (int j = x0 * kItemKeys; j < min(x1 * kItemKeys, min(pos + 1, u.nk)); ++j) {
-                            const int pg = page_of(c, w.b, j / c.page_size);
+                    {
+                        const int pf = w->sq.pos0 + w->u.tok0;  // tiles that end past it were cleared
+                        const int x0 = max(first, max(0, pf + 1) / kItemKeys), x1 = min(end, n_seq);
+                        for (int j = x0 * kItemKeys; j < min(x1 * kItemKeys, min(pos + 1, w->u.nk)); ++j) {
+                            const int pg = page_of(c, w->b, j / c.page_size);
                             if (pg >= 0)
-                                add(p.v_pages + (((long long)pg * c.Hkv + w.kvh) * c.page_size + j % c.page_size) * kD);
+                                add(p.v_pages + (((long long)pg * c.Hkv + kvh) * c.page_size + j % c.page_size) * kD);
                         }
                     }
                     for (int s = 0; s < p.Ld; ++s) {
-                        const int xi = u.n_seq + (tl * p.DSL + s / 16) / kSlices;
-                        if (xi >= w.first && xi < w.end)
-                            add(p.vd + (((long long)(w.sq.q0 + u.tok0 + tl) * p.Ld_cap + s) * c.Hkv + w.kvh) * kD);
+                        const int xi = n_seq + (tl * p.DSL + s / 16) / kSlices;
+                        if (xi >= first && xi < end)
+                            add(p.vd + (((long long)(w->sq.q0 + w->u.tok0 + tl) * p.Ld_cap + s) * c.Hkv + kvh) * kD);
                     }
                 }
                 if (!valid) continue;
@@ -740,12 +724,18 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
 #pragma unroll
                     for (int v = 0; v < 4; ++v) dst[v] = make_uint4(q[4 * v], q[4 * v + 1], q[4 * v + 2], q[4 * v + 3]);
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(p.part_o + ((long long)ps * kRows + i * 128 + r) * kD + cc * 32);
+                    float* dst = p.part_o + ((long long)ps * kRows + i * 128 + r) * kD + cc * 32;
 #pragma unroll
-                    for (int v = 0; v < 8; ++v) dst[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                    for (int v = 0; v < 4; ++v) ptx::st_global_32b(dst + 8 * v, &o[8 * v]);
                 }
             }
             if (valid) {
+                if (!whole && first == 0 && threadIdx.x == 0) {
+                    // parts of the unit, up to the one that holds its last item
+                    const long long last = bars->hi - w->left + w->u.n_items;
+                    const int c_last = (int)((last * bars->W + bars->total - 1) / bars->total) - 1;
+                    p.desc[cta] = make_int4(w->b, kvh, w->rt, (c_last - cta + 1) | min(w->u.ntok * p.G, kRows) << 16);
+                }
                 if (!whole)
                     *reinterpret_cast<float2*>(p.part_ml + ((long long)ps * kRows + i * 128 + r) * 2) = make_float2(m, l);
                 else if (p.lse)
@@ -766,13 +756,13 @@ __global__ void __launch_bounds__(Roles<Q8>::kThreads, 1) paged_pre_kernel(const
     }
 }
 
-template <bool Q8>
-cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
+cudaError_t launch(const PagedFwdArgs& a, char* ws, cudaStream_t s) {
     PreParams p;
     memset(static_cast<void*>(&p), 0, sizeof(p));
     const PagedCache& c = a.c;
-    const cuuint64_t P = c.page_size, Hkv = c.Hkv, e = Q8 ? 1 : 2;
+    const cuuint64_t P = c.page_size, Hkv = c.Hkv;
     p.n = 128 / a.G;
+    for (p.lg_step = 0; (1 << p.lg_step) < 2 * p.n;) ++p.lg_step;
     {
         const cuuint64_t dims[4] = {kD, (cuuint64_t)a.Hq, (cuuint64_t)c.N, 1};
         const cuuint64_t st[3] = {kD * 2, (cuuint64_t)a.Hq * kD * 2, (cuuint64_t)c.N * a.Hq * kD * 2};
@@ -781,11 +771,11 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
     }
     {
         const cuuint64_t dims[4] = {kD, P, Hkv, (cuuint64_t)c.num_pages};
-        const cuuint64_t st[3] = {kD * e, P * kD * e, Hkv * P * kD * e};
-        const cuuint32_t box[4] = {Q8 ? 128u : 64u, 16, 1, 1};
-        const bool ok = Q8 ? make_tmap_u8_4d(&p.tm_k, a.k_pages, dims, st, box) && make_tmap_u8_4d(&p.tm_v, a.v_pages, dims, st, box)
-                           : make_tmap_bf16_4d(&p.tm_k, a.k_pages, dims, st, box) && make_tmap_bf16_4d(&p.tm_v, a.v_pages, dims, st, box);
-        if (!ok) return cudaErrorInvalidValue;
+        const cuuint64_t st[3] = {kD * 2, P * kD * 2, Hkv * P * kD * 2};
+        p.box_rows = std::min(c.page_size & -c.page_size, kItemKeys);
+        const cuuint32_t box[4] = {64, (cuuint32_t)p.box_rows, 1, 1};
+        if (!make_tmap_bf16_4d(&p.tm_k, a.k_pages, dims, st, box) || !make_tmap_bf16_4d(&p.tm_v, a.v_pages, dims, st, box))
+            return cudaErrorInvalidValue;
     }
     if (a.Ld > 0) {
         const cuuint64_t dims[4] = {kD, Hkv, (cuuint64_t)a.Ld, (cuuint64_t)c.N};
@@ -798,9 +788,7 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
         p.tm_vd = p.tm_v;
     }
     p.c = c;
-    p.k_scale = a.k_scale;
-    p.v_scale = a.v_scale;
-    p.v_pages = Q8 ? nullptr : static_cast<const __nv_bfloat16*>(a.v_pages);
+    p.v_pages = static_cast<const __nv_bfloat16*>(a.v_pages);
     p.vd = static_cast<const __nv_bfloat16*>(a.vd);
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.lse = a.lse;
@@ -808,19 +796,68 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
     p.sl2 = a.scale * 1.4426950408889634f;
     p.status = a.status;
     p.wait_limit = a.wait_limit;
-    char* ws = static_cast<char*>(a.workspace);
     p.desc = reinterpret_cast<int4*>(ws);
+    // [desc | part_ml | part_o], part_o at a 32-byte boundary
     p.part_ml = reinterpret_cast<float*>(ws + kParts * sizeof(int4));
-    p.part_o = p.part_ml + (size_t)2 * kParts * kRows * 2;
-    auto kern = paged_pre_kernel<Q8>;
+    p.part_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(p.part_ml + (size_t)2 * kParts * kRows * 2) + 31) & ~uintptr_t(31));
     static SmemLimit limit;
-    cudaError_t err = limit.raise(reinterpret_cast<const void*>(kern), kSmemBytes);
+    cudaError_t err = limit.raise(reinterpret_cast<const void*>(paged_pre_kernel), kSmemBytes);
     if (err != cudaSuccess) return err;
-    kern<<<kParts, Roles<Q8>::kThreads, kSmemBytes, s>>>(p);
+    paged_pre_kernel<<<kParts, kThreads, kSmemBytes, s>>>(p);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     JoinParams j{p.c, p.out, p.lse, p.part_o, p.part_ml, p.desc, p.Hq, p.G};
     return launch_paged_join<kRows, kD, kParts>(j, s);
+}
+
+// 8-bit pages to bf16 pages of the same numbering, for the pages this call
+// reads: value = code * scale, exact, as the scale is a power of two. Every
+// unit of a chunk would otherwise convert the same tiles again: in the kernel
+// the conversion shared the SM with the softmax and took two and a half times
+// the matrix products' time, here it is one pass over the cache (1 byte read,
+// 2 written per element), and what it writes is still in L2 when it is read.
+// One CTA per (block of the table, kv-head): 16 codes per thread and step.
+__global__ void __launch_bounds__(256) paged_dequant_kernel(const PagedCache c, const int8_t* kc, const int8_t* vc,
+                                                            const float* ks, const float* vs, __nv_bfloat16* ko,
+                                                            __nv_bfloat16* vo) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int h = blockIdx.y;
+    const int total = c.B * c.max_blocks;
+    for (int x = blockIdx.x; x < total; x += gridDim.x) {
+        const int b = x / c.max_blocks, blk = x % c.max_blocks;
+        const SeqInfo s = seq_info(c, b);
+        const long long keys = (long long)s.pos0 + s.n;  // seen by the last new token
+        if (s.n == 0 || (long long)blk * c.page_size >= keys) continue;
+        const int page = page_of(c, b, blk);
+        if (page < 0) continue;
+        const long long row = (long long)page * c.Hkv + h;
+        const float k1 = __ldg(ks + row), v1 = __ldg(vs + row);
+        const long long at = row * c.page_size * kD;
+        const int n16 = (int)min((long long)c.page_size, keys - (long long)blk * c.page_size) * (kD / 16);
+        for (int e = threadIdx.x; e < n16; e += blockDim.x) {
+            const uint4 a = *reinterpret_cast<const uint4*>(kc + at + e * 16), d = *reinterpret_cast<const uint4*>(vc + at + e * 16);
+            auto put = [&](const uint4& w, float sc, __nv_bfloat16* dst) {
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int i0 = (int)(u[q] << 24) >> 24, i1 = (int)(u[q] << 16) >> 24, i2 = (int)(u[q] << 8) >> 24, i3 = (int)u[q] >> 24;
+                    o[2 * q] = ptx::pack_bf16x2(i0 * sc, i1 * sc);
+                    o[2 * q + 1] = ptx::pack_bf16x2(i2 * sc, i3 * sc);
+                }
+                ptx::st_global_32b(dst, o);
+            };
+            put(a, k1, ko + at + e * 16);
+            put(d, v1, vo + at + e * 16);
+        }
+    }
+}
+
+size_t join_bytes() {
+    return kParts * sizeof(int4) + 2 * (size_t)kParts * kRows * (kD + 2) * sizeof(float) + 32;
+}
+size_t pool_bytes(int Hkv, long long num_pages, int page_size) {
+    return ((size_t)num_pages * Hkv * page_size * kD * 2 + 255) & ~size_t(255);
 }
 
 }  // namespace
@@ -832,12 +869,29 @@ bool paged_pre_supported(const PagedFwdArgs& a) {
            (long long)a.c.N * a.Hq < (1LL << 31);
 }
 
-size_t paged_pre_workspace() {
-    return kParts * sizeof(int4) + 2 * (size_t)kParts * kRows * (kD + 2) * sizeof(float);
+size_t paged_pre_workspace(int Hkv, long long num_pages, int page_size, bool q8) {
+    const size_t parts = (join_bytes() + 255) & ~size_t(255);
+    return q8 ? parts + 2 * pool_bytes(Hkv, num_pages, page_size) + 32 : parts;
 }
 
 cudaError_t launch_paged_pre(const PagedFwdArgs& a, cudaStream_t s) {
-    return a.k_scale ? launch<true>(a, s) : launch<false>(a, s);
+    char* ws = static_cast<char*>(a.workspace);
+    if (!a.k_scale) return launch(a, ws, s);
+    // [parts | bf16 K pages | bf16 V pages], the pages at 32-byte boundaries
+    const PagedCache& c = a.c;
+    char* pages = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws + ((join_bytes() + 255) & ~size_t(255))) + 31) & ~uintptr_t(31));
+    const size_t pool = pool_bytes(c.Hkv, c.num_pages, c.page_size);
+    PagedFwdArgs f = a;
+    f.k_pages = pages;
+    f.v_pages = pages + pool;
+    f.k_scale = f.v_scale = nullptr;
+    const long long blocks = (long long)c.B * c.max_blocks;
+    if (blocks > 0x7fffffffLL || c.Hkv > 65535) return cudaErrorInvalidValue;
+    paged_dequant_kernel<<<dim3((unsigned)std::min(blocks, 4096LL), c.Hkv), 256, 0, s>>>(
+        c, static_cast<const int8_t*>(a.k_pages), static_cast<const int8_t*>(a.v_pages), a.k_scale, a.v_scale,
+        reinterpret_cast<__nv_bfloat16*>(pages), reinterpret_cast<__nv_bfloat16*>(pages + pool));
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? launch(f, ws, s) : e;
 }
 
 }  // namespace moda

@@ -440,14 +440,19 @@ moda_status moda_paged_append_q8(const void* q, const void* k, const void* v,
  *                  the kernel, results do not depend on its being right
  *   workspace  in  device scratch of >= moda_fwd_paged_workspace_bytes(...),
  *                  16-byte aligned, contents on entry ignored (may be NULL
- *                  when that is 0). Calls that share it must not overlap.
+ *                  when that is 0). Calls that share it must not overlap. For
+ *                  chunks over 8-bit pages (max_q * G of 65 and more, d = 128;
+ *                  q8 != 0 in the size's call) it also holds the pages in use
+ *                  as bf16, in two pools of num_pages pages; one workspace
+ *                  serves all layers.
  * The attention does not append: call moda_paged_append first, with the same
  * cu_q, ctx_lens and block_table. moda_fwd_paged_q8 reads 8-bit pages; depth
  * rows stay in `dtype`. bf16 with d % 8 == 0 and page_size % 16 == 0 runs on
  * the tensor cores, everything else on the SIMT kernels (MODA_IMPL_TC2 is not
  * offered: MODA_ERR_UNSUPPORTED). Errors otherwise as moda_fwd_ex.
  */
-size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d, moda_dtype dtype);
+size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d,
+                                      int num_pages, int page_size, moda_dtype dtype, int q8);
 moda_status moda_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
                            const void* kd, const void* vd,
                            const int32_t* cu_q, const int32_t* ctx_lens, const int32_t* block_table,

@@ -63,13 +63,18 @@ def test_fwd_refusals(kw, code):
 
 
 def test_workspace_refusals():
-    n = moda._c_paged_ws(4, 2, 2, 8, 2, 128, 0)
-    if n:
-        assert fwd(ws=None) == 4
-        assert fwd(nws=n - 1) == 4
-        assert fwd(ws=P + 8) == 3
-    assert moda._c_paged_ws(0, 2, 2, 8, 2, 128, 0) == 0
-    assert moda._c_paged_ws(4, 2, 2, 7, 2, 128, 0) == 0
+    n = moda._c_paged_ws(4, 2, 2, 8, 2, 128, 5, 16, 0, 0)
+    assert n > 0
+    assert fwd(ws=None) == 4
+    assert fwd(nws=n - 1) == 4
+    assert fwd(ws=P + 8) == 3
+    # chunks over 8-bit pages: two bf16 pools beside the parts of cut units
+    a, b = (moda._c_paged_ws(99, 2, 90, 8, 2, 128, 1000, 16, 0, q8) for q8 in (0, 1))
+    assert b - a >= 2 * 1000 * 2 * 16 * 128 * 2
+    assert fwd(max_q=90, N=99, pages=1000, nws=b - 1, scales=(P, P)) == 4
+    for bad in ((0, 2, 2, 8, 2, 128, 5, 16, 0, 0), (4, 2, 2, 7, 2, 128, 5, 16, 0, 0), (4, 2, 2, 8, 2, 128, 0, 16, 0, 0)):
+        assert moda._c_paged_ws(*bad) == 0
+    assert moda._c_paged_ws(4, 2, 2, 8, 2, 128, 5, 16, 1, 0) == 0  # fp32 needs none
 
 
 def cpu_call():

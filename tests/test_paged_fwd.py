@@ -136,7 +136,8 @@ def test_twice_the_same_and_shared_workspace(q8):
     holds NaN; two captured graphs that share it replay one after the other."""
     c = Paged("again", ((3000, 1), (1500, 2), (10, 1)), Hq=32, Hkv=4, Ld=6, cap=6)
     x = cuda(make(c, q8=q8))
-    n = moda.moda_fwd_paged_workspace_bytes(c.N, len(c.seqs), x["max_q"], c.Hq, c.Hkv, c.d, torch.bfloat16)
+    n = moda.moda_fwd_paged_workspace_bytes(c.N, len(c.seqs), x["max_q"], c.Hq, c.Hkv, c.d,
+                                            x["k_pages"].shape[0], c.P, torch.bfloat16, q8)
     ws = torch.full((max(n, 16) // 4,), float("nan"), device="cuda").view(torch.uint8)
     a = run(x, c, q8)
     b = run(x, c, q8, workspace=ws)
