@@ -1,7 +1,8 @@
 """Python binding of the MoDA C ABI (``libmoda.so``, header ``include/moda.h``).
 
 Argument marshalling only: every function forwards torch CUDA tensors' device
-pointers and the current CUDA stream to the C entry point of the same name.
+pointers and the current CUDA stream to the C entry point of the same name
+(the paged-cache functions through a compiled binding, the others by ctypes).
 All arithmetic runs in the library's CUDA kernels. There is no CPU fallback:
 importing this package fails if the library has not been built
 (``python depth_kv_attention_b200/csrc/build.py``).
@@ -13,9 +14,7 @@ lse [N,Hq], pages [num_pages,Hkv,page_size,d].
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-import functools
 import math
 import os
 
@@ -37,6 +36,11 @@ if not os.path.exists(LIB_PATH):
         f"{LIB_PATH} is missing: build it with `python depth_kv_attention_b200/csrc/build.py` "
         "(the MoDA path has no CPU fallback)")
 lib = ctypes.CDLL(LIB_PATH)
+try:
+    from . import _moda_torch as _bind  # the paged-cache entry points on tensors
+except ImportError as e:
+    raise ImportError(f"depth_kv_attention_b200/_moda_torch.so does not load ({e}): build it with "
+                      "`python depth_kv_attention_b200/csrc/build.py`") from e
 
 MODA_OK = 0
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
@@ -76,14 +80,7 @@ _c_fwd_q8 = _sig("moda_fwd_q8", _i, [_vp] * 7 + _DIMS + [_i, _f, _vp, _vp, _vp, 
 _c_quant_q8 = _sig("moda_depth_quantize_q8", _i, [_vp, _vp] + [_i] * 5 + [_i] + [_vp] * 4 + [_vp])
 _c_write_q8 = _sig("moda_depth_write_q8", _i, [_vp, _vp] + [_i] * 6 + [_i] + [_vp] * 4 + [_vp])
 _c_fwd_host = _sig("moda_fwd_host", _i, [_vp] * 5 + _DIMS + [_i, _f, _vp, _vp, _vp, _sz, _vp])
-_ll = ctypes.c_longlong
-_APPEND = [_vp] * 3 + [_ll] * 3 + [_vp, _i, _i, _i] + [_vp] * 3 + [_i] * 9
-_c_append = _sig("moda_paged_append", _i, _APPEND + [_vp] * 5 + [_i, _i, _vp])
-_c_append_q8 = _sig("moda_paged_append_q8", _i, _APPEND + [_vp] * 7 + [_i, _i, _vp])
 _c_paged_ws = _sig("moda_fwd_paged_workspace_bytes", _sz, [_i] * 10)
-_PAGED = [_vp] * 5 + [_i] * 12 + [_f, _vp, _vp, _vp, _sz, _vp, _i]
-_c_fwd_paged = _sig("moda_fwd_paged", _i, [_vp] * 3 + _PAGED)
-_c_fwd_paged_q8 = _sig("moda_fwd_paged_q8", _i, [_vp] * 5 + _PAGED)
 
 
 class ModaError(RuntimeError):
@@ -389,95 +386,15 @@ def depth_slot_view(kd, slot: int):
     return kd.as_strided((B, T, Hkv, d), st, kd.storage_offset() + off)
 
 
-def _on(device):
-    """Guard that makes ``device`` current; free when it is already."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _result(r, where):
+    """A binding function's result; a status code becomes a ModaError."""
+    if type(r) is int:
+        raise ModaError(r, where)
+    return r
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _check_cache(where, q, k_pages, v_pages, scales, block_table, cu_q, ctx_lens, kd, vd, *others):
-    """Shapes, types and places of the arguments that both paged operators
-    share. Returns (N, B, Hq, Hkv, d, num_pages, page_size, max_blocks)."""
-    if q.dim() != 3 or k_pages.dim() != 4 or block_table.dim() != 2:
-        raise ValueError(f"{where}: packed tokens [N,H,d], pages [num_pages,Hkv,page_size,d] and a block table "
-                         "[B,max_blocks] expected")
-    N, Hq, d = q.shape
-    num_pages, Hkv, page_size, dp = k_pages.shape
-    B, max_blocks = block_table.shape
-    if dp != d or v_pages.shape != k_pages.shape or cu_q.shape != (B + 1,) or ctx_lens.shape != (B,):
-        raise ValueError(f"{where}: shapes of pages, cu_q [B+1] or ctx_lens [B] do not match")
-    if not (cu_q.dtype == ctx_lens.dtype == block_table.dtype == torch.int32):
-        raise ValueError(f"{where}: int32 cu_q, ctx_lens and block_table expected")
-    if q.dtype not in _DTYPE:
-        raise ValueError(f"{where}: bf16 or fp32 expected")
-    want = q.dtype if scales is None else torch.int8
-    if k_pages.dtype != want or v_pages.dtype != want:
-        raise ValueError(f"{where}: pages of {want} expected")
-    if scales is not None:
-        for t in scales:
-            if t.dtype != torch.float32 or t.shape != (num_pages, Hkv):
-                raise ValueError(f"{where}: fp32 scales [num_pages,Hkv] expected")
-    if (kd is None) != (vd is None):
-        raise ValueError(f"{where}: kd and vd come together")
-    if kd is not None and (kd.dim() != 4 or kd.shape[0] != N or kd.shape[2:] != (Hkv, d) or kd.shape != vd.shape
-                           or kd.dtype != q.dtype or vd.dtype != q.dtype):
-        raise ValueError(f"{where}: kd, vd [N,Ld,Hkv,d] of the tokens' type expected")
-    dev = q.device
-    for t in (k_pages, v_pages, block_table, cu_q, ctx_lens, kd, vd, *(scales or ()), *others):
-        if t is not None and not (t.is_contiguous() and t.device == dev):
-            raise ValueError(f"{where}: contiguous tensors on one device expected")
-    if not q.is_cuda:
-        raise ValueError("MoDA tensors must be CUDA tensors")
-    return N, B, Hq, Hkv, d, num_pages, page_size, max_blocks
-
-
-def _token_stride(where, t, device):
-    """Elements from token to token of t [N,H,d] with dense heads (a dimension
-    of one element may carry any stride)."""
-    N, H, d = t.shape
-    if t.device != device or (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d):
-        raise ValueError(f"{where}: dense heads on one device expected (any stride from token to token)")
-    return t.stride(0) if N > 1 else H * d
-
-
-def _append(where, fn, q, k, v, pages, scales, block_table, cu_q, ctx_lens, rope, interleaved, q_out, kd, vd, slot,
-            stream):
-    N, B, Hk, Hkv, d, num_pages, page_size, max_blocks = _check_cache(
-        where, k, pages[0], pages[1], scales, block_table, cu_q, ctx_lens, kd, vd, rope, q_out)
-    if Hk != Hkv or v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError(f"{where}: k, v [N,Hkv,d] of one type expected")
-    Hq = Hkv
-    if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else 0
-        if q.shape != (N, Hq, d) or q.dtype != k.dtype:
-            raise ValueError(f"{where}: q [N,Hq,d] of the type of k expected")
-        if q_out is None:
-            q_out = torch.empty((N, Hq, d), device=q.device, dtype=q.dtype)
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype:
-            raise ValueError(f"{where}: q_out like q expected")
-    elif q_out is not None:
-        raise ValueError(f"{where}: q_out without q")
-    strides = [0 if t is None else _token_stride(where, t, k.device) for t in (q, k, v)]
-    if rope is not None and (rope.dtype != torch.float32 or rope.dim() != 2):
-        raise ValueError(f"{where}: fp32 rope [positions, rot_dim] expected")
-    if N == 0:
-        return q_out
-    with _on(k.device):
-        _check(fn(_addr(q), k.data_ptr(), v.data_ptr(), *strides, _addr(rope),
-                  0 if rope is None else rope.shape[0], 0 if rope is None else rope.shape[1], int(interleaved),
-                  cu_q.data_ptr(), ctx_lens.data_ptr(), block_table.data_ptr(), N, B, Hq, Hkv, d, num_pages, page_size,
-                  max_blocks, _DTYPE[k.dtype], pages[0].data_ptr(), pages[1].data_ptr(),
-                  *(t.data_ptr() for t in scales or ()), _addr(q_out), _addr(kd), _addr(vd),
-                  0 if kd is None else kd.shape[1], slot, _stream_addr(stream)), where)
-    return q_out
-
-
-def _stream_addr(stream):
-    # the raw handle: making a Stream object costs as much as a launch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def moda_paged_append(q, k, v, k_pages, v_pages, block_table, cu_q, ctx_lens, rope=None, interleaved: bool = False,
@@ -486,11 +403,11 @@ def moda_paged_append(q, k, v, k_pages, v_pages, block_table, cu_q, ctx_lens, ro
     k [N,Hkv,d], rotated by each token's position, and v into k_pages, v_pages
     [num_pages,Hkv,page_size,d], in place; with kd, vd [N,Ld,Hkv,d] also into
     depth slot ``slot``. q (may be None), k and v need dense heads only, so
-    column blocks of one projection's output serve as they are. ``rope`` [positions, rot_dim]
-    holds cos | sin rows; None leaves q and k unrotated. Returns the rotated q
-    (``q_out`` when given; None without q)."""
-    return _append("moda_paged_append", _c_append, q, k, v, (k_pages, v_pages), None, block_table, cu_q, ctx_lens,
-                   rope, interleaved, q_out, kd, vd, slot, stream)
+    column blocks of one projection's output serve as they are. ``rope``
+    [positions, rot_dim] holds cos | sin rows; None leaves q and k unrotated.
+    Returns the rotated q (``q_out`` when given; None without q)."""
+    return _result(_bind.paged_append(q, k, v, k_pages, v_pages, None, None, block_table, cu_q, ctx_lens, rope,
+                                      interleaved, q_out, kd, vd, slot, _handle(stream)), "moda_paged_append")
 
 
 def moda_paged_append_q8(q, k, v, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens, rope=None,
@@ -498,54 +415,14 @@ def moda_paged_append_q8(q, k, v, k_pages, v_pages, k_scale, v_scale, block_tabl
     """``moda_paged_append`` into 8-bit pages (``moda_paged_append_q8``): int8
     codes k_pages, v_pages and fp32 power-of-two scales [num_pages,Hkv], in
     place. kd, vd stay in the tokens' type."""
-    return _append("moda_paged_append_q8", _c_append_q8, q, k, v, (k_pages, v_pages), (k_scale, v_scale), block_table,
-                   cu_q, ctx_lens, rope, interleaved, q_out, kd, vd, slot, stream)
-
-
-@functools.lru_cache(maxsize=256)
-def _paged_ws(*dims):
-    return _c_paged_ws(*dims)
+    if k_scale is None or v_scale is None:
+        raise ValueError("moda_paged_append_q8: fp32 scales [num_pages,Hkv] expected")
+    return _result(_bind.paged_append(q, k, v, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens, rope,
+                                      interleaved, q_out, kd, vd, slot, _handle(stream)), "moda_paged_append_q8")
 
 
 def moda_fwd_paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, num_pages, page_size, dtype, q8: bool = False) -> int:
     return _c_paged_ws(N, B, max_q, Hq, Hkv, d, num_pages, page_size, _DTYPE[dtype], int(q8))
-
-
-def _fwd_paged(where, fn, q, pages, scales, block_table, cu_q, ctx_lens, max_q, kd, vd, Ld, scale, out, lse,
-               workspace, impl, stream):
-    N, B, Hq, Hkv, d, num_pages, page_size, max_blocks = _check_cache(
-        where, q, pages[0], pages[1], scales, block_table, cu_q, ctx_lens, kd, vd, q, out, lse, workspace)
-    cap = 0 if kd is None else kd.shape[1]
-    if Ld is None:
-        Ld = cap
-    if not 0 <= Ld <= cap:
-        raise ValueError(f"{where}: Ld must lie in [0, slots of kd]")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    if out is None:
-        out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError(f"{where}: out like q expected")
-    if lse is None:
-        lse = torch.empty((N, Hq), device=q.device, dtype=torch.float32)
-    elif lse.shape != (N, Hq) or lse.dtype != torch.float32:
-        raise ValueError(f"{where}: fp32 lse [N,Hq] expected")
-    if N == 0:
-        return out, lse
-    dt = _DTYPE[q.dtype]
-    need = _paged_ws(N, B, max_q, Hq, Hkv, d, num_pages, page_size, dt, scales is not None)
-    with _on(q.device):
-        if workspace is None and need:
-            # from the pool of the stream it is used on
-            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-                workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
-        _check(fn(q.data_ptr(), pages[0].data_ptr(), pages[1].data_ptr(), *(t.data_ptr() for t in scales or ()),
-                  _addr(kd) if Ld else None, _addr(vd) if Ld else None, cu_q.data_ptr(), ctx_lens.data_ptr(),
-                  block_table.data_ptr(), N, B, max_q, Hq, Hkv, d, Ld, cap, num_pages, page_size, max_blocks, dt,
-                  scale, out.data_ptr(), lse.data_ptr(), _addr(workspace),
-                  0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_addr(stream),
-                  _IMPL[impl]), where)
-    return out, lse
 
 
 def moda_fwd_paged(q, k_pages, v_pages, block_table, cu_q, ctx_lens, max_q: int, kd=None, vd=None,
@@ -555,10 +432,10 @@ def moda_fwd_paged(q, k_pages, v_pages, block_table, cu_q, ctx_lens, max_q: int,
     [N,Hq,d] of the new tokens against their sequences' pages and, under the
     same softmax, slots 0..Ld-1 (default all) of their own depth rows kd, vd
     [N,slots,Hkv,d]. ``max_q``: about the most new tokens of any sequence.
-    ``workspace``: a uint8 CUDA tensor of moda_fwd_paged_workspace_bytes, made
+    ``workspace``: a CUDA tensor of moda_fwd_paged_workspace_bytes bytes, made
     here when not given. Returns (out [N,Hq,d], lse [N,Hq])."""
-    return _fwd_paged("moda_fwd_paged", _c_fwd_paged, q, (k_pages, v_pages), None, block_table, cu_q, ctx_lens, max_q,
-                      kd, vd, Ld, scale, out, lse, workspace, impl, stream)
+    return _result(_bind.fwd_paged(q, k_pages, v_pages, None, None, block_table, cu_q, ctx_lens, max_q, kd, vd, Ld, scale,
+                                   out, lse, workspace, _IMPL[impl], _handle(stream)), "moda_fwd_paged")
 
 
 def moda_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens, max_q: int, kd=None,
@@ -566,8 +443,10 @@ def moda_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, 
                       impl: str = "auto", stream=None):
     """``moda_fwd_paged`` over 8-bit pages (``moda_fwd_paged_q8``): int8 codes
     and fp32 scales [num_pages,Hkv], as moda_paged_append_q8 writes them."""
-    return _fwd_paged("moda_fwd_paged_q8", _c_fwd_paged_q8, q, (k_pages, v_pages), (k_scale, v_scale), block_table,
-                      cu_q, ctx_lens, max_q, kd, vd, Ld, scale, out, lse, workspace, impl, stream)
+    if k_scale is None or v_scale is None:
+        raise ValueError("moda_fwd_paged_q8: fp32 scales [num_pages,Hkv] expected")
+    return _result(_bind.fwd_paged(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens, max_q, kd, vd, Ld,
+                                   scale, out, lse, workspace, _IMPL[impl], _handle(stream)), "moda_fwd_paged_q8")
 
 
 def moda_device_status(stream=None) -> int:

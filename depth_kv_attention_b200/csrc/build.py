@@ -9,6 +9,10 @@ the object is newer than its source and every header); the objects link into
 ``depth_kv_attention_b200/libmoda.so``. The CUDA runtime is linked statically;
 the driver entry point for tensor-map encoding is fetched at run time, so the
 library needs no ``libcuda`` at link time.
+
+``csrc/bind_torch.cpp`` (the binding of the paged-cache entry points on torch
+tensors) compiles with g++ against torch's headers into
+``depth_kv_attention_b200/_moda_torch.so``, which links to libmoda.so.
 """
 from __future__ import annotations
 
@@ -25,6 +29,8 @@ PKG = os.path.dirname(CSRC)
 ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoda.so")
+BIND_SRC = os.path.join(CSRC, "bind_torch.cpp")
+BIND = os.path.join(PKG, "_moda_torch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -74,14 +80,43 @@ def build(verbose: bool = False, force: bool = False, extra: list[str] | None = 
         with cf.ThreadPoolExecutor(max_workers=min(8, len(todo))) as ex:
             list(ex.map(lambda s: _compile(s, verbose, extra), todo))
     if todo or not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs):
-        cmd = [nvcc()] + ARCH + ["-shared", "-o", LIB + ".tmp"] + objs + ["-cudart", "static"]
+        cmd = [nvcc()] + ARCH + ["-shared", "-o", LIB + ".tmp"] + objs + ["-cudart", "static",
+                                                                         "-Xlinker", "-soname=libmoda.so"]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(LIB + ".tmp", LIB)
+    build_binding(verbose, force)
     return LIB
+
+
+def build_binding(verbose: bool = False, force: bool = False) -> str:
+    """Compile the torch binding (after libmoda.so). Returns its path."""
+    header = os.path.join(ROOT, "include", "moda.h")
+    if not force and os.path.exists(BIND) and all(os.path.getmtime(f) <= os.path.getmtime(BIND)
+                                                  for f in (BIND_SRC, header)):
+        return BIND
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+           + [x for i in inc for x in ("-isystem", i)]
+           + [BIND_SRC, "-o", BIND + ".tmp", "-L" + lib, "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10",
+              "-lc10_cuda", "-L" + PKG, "-l:libmoda.so", "-Wl,-rpath,$ORIGIN"])
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(BIND + ".tmp", BIND)
+    return BIND
 
 
 def main(argv=None) -> int:

@@ -573,6 +573,7 @@ moda_status run_append(const void* q, const void* k, const void* v, long long sq
     a.Hq = Hq; a.dtype = dtype;
     a.q_out = q_out; a.k_pages = k_pages; a.v_pages = v_pages; a.k_scale = k_scale; a.v_scale = v_scale;
     a.kd = kd; a.vd = vd; a.Ld = Ld; a.slot = slot;
+    if (status_ptr(&a.status, &a.wait_limit) != cudaSuccess) return MODA_ERR_CUDA;
     return launch_paged_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MODA_OK : MODA_ERR_LAUNCH;
 }
 

@@ -40,6 +40,8 @@ struct AppendArgs {
     void* kd;  // [N, Ld, Hkv, d] or null
     void* vd;
     int Ld, slot;
+    unsigned int* status;     // device status word
+    unsigned int wait_limit;  // bounded-wait polls (0 = default)
 };
 
 struct PagedFwdArgs {

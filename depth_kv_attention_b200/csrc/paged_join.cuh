@@ -1,13 +1,13 @@
 // Joining the parts of work units that the paged attention kernels cut (see
-// paged_units.cuh), and the host side both kernels share.
+// paged_units.cuh).
 #pragma once
 
-#include <atomic>
 #include <cmath>
 #include <cstring>
 
 #include "paged_units.cuh"
 #include "sm100_ptx.cuh"
+#include "smem_limit.h"
 
 namespace moda {
 
@@ -146,22 +146,5 @@ cudaError_t launch_paged_join(const JoinParams& p, cudaStream_t s) {
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, paged_join_kernel<MR, D, W>, p);
 }
-
-// Raises a kernel's dynamic shared memory limit once per device (the call
-// costs more than a launch). A device reset in between is noticed by the
-// launch, which then fails; the attribute is set again on the next call.
-struct SmemLimit {
-    std::atomic<unsigned long long> done{0};
-    cudaError_t raise(const void* kernel, int bytes) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        const unsigned long long bit = 1ull << (dev & 63);
-        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-        return e;
-    }
-};
 
 }  // namespace moda

@@ -113,6 +113,14 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_lead(uint64_t* bar, uint32
         "r"(bytes), "r"(leader)
         : "memory");
 }
+// Untiled bulk copy into this CTA's shared memory: both addresses 16-byte
+// aligned, a multiple of 16 bytes; completion counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
 // 4-D tiled load into shared memory, completion counted on `bar` (bytes).
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0,
                                             int c1, int c2, int c3) {

@@ -1,11 +1,29 @@
 """Refusals of the paged cache's entry points, decided before any CUDA call
 (fake 16-byte aligned addresses, never dereferenced), and those of the Python
 binding on CPU tensors."""
+import ctypes
+
 import pytest
 import torch
 
 moda = pytest.importorskip("depth_kv_attention_b200",
                            reason="libmoda.so not built (python depth_kv_attention_b200/csrc/build.py)")
+
+_vp, _i, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
+
+
+def entry(name, args):
+    fn = getattr(moda.lib, name)
+    fn.restype, fn.argtypes = _i, args
+    return fn
+
+
+_APPEND = [_vp] * 3 + [_ll] * 3 + [_vp, _i, _i, _i] + [_vp] * 3 + [_i] * 9
+_FWD = [_vp] * 5 + [_i] * 12 + [ctypes.c_float, _vp, _vp, _vp, ctypes.c_size_t, _vp, _i]
+c_append = entry("moda_paged_append", _APPEND + [_vp] * 5 + [_i, _i, _vp])
+c_append_q8 = entry("moda_paged_append_q8", _APPEND + [_vp] * 7 + [_i, _i, _vp])
+c_fwd_paged = entry("moda_fwd_paged", [_vp] * 3 + _FWD)
+c_fwd_paged_q8 = entry("moda_fwd_paged_q8", [_vp] * 5 + _FWD)
 
 P = 0x10000
 DIMS = dict(N=4, B=2, Hq=8, Hkv=2, d=128, pages=5, page=16, blocks=3, dt=0)
@@ -17,8 +35,8 @@ def append(q=P, k=P, v=P, sq=1024, sk=256, sv=256, rope=P, rope_len=64, rot=128,
     dims = [x["N"], x["B"], x["Hq"], x["Hkv"], x["d"], x["pages"], x["page"], x["blocks"], x["dt"]]
     args = [q, k, v, sq, sk, sv, rope, rope_len, rot, 0, cu, ctx, table, *dims, kp, vp]
     if scales is None:
-        return moda._c_append(*args, qo, kd, vd, Ld, slot, None)
-    return moda._c_append_q8(*args, *scales, qo, kd, vd, Ld, slot, None)
+        return c_append(*args, qo, kd, vd, Ld, slot, None)
+    return c_append_q8(*args, *scales, qo, kd, vd, Ld, slot, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -44,8 +62,8 @@ def fwd(q=P, kp=P, vp=P, kd=P, vd=P, cu=P, ctx=P, table=P, max_q=2, Ld=2, cap=4,
     tail = [kd, vd, cu, ctx, table, x["N"], x["B"], max_q, x["Hq"], x["Hkv"], x["d"], Ld, cap, x["pages"], x["page"],
             x["blocks"], x["dt"], scale, out, lse, ws, nws, None, impl]
     if scales is None:
-        return moda._c_fwd_paged(q, kp, vp, *tail)
-    return moda._c_fwd_paged_q8(q, kp, vp, *scales, *tail)
+        return c_fwd_paged(q, kp, vp, *tail)
+    return c_fwd_paged_q8(q, kp, vp, *scales, *tail)
 
 
 @pytest.mark.parametrize("kw,code", [

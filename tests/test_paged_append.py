@@ -28,6 +28,12 @@ CASES = [
     Paged("no_rot", ((300, 300), (5, 2)), d=8, P=64, Hq=5, Hkv=5, cap=2),
     Paged("f32", ((130, 129), (64, 1), (65, 2)), d=128, dtype="f32", rot=128, P=64, Hq=16, Hkv=2, cap=1),
     Paged("f32_small", ((9, 9), (12, 4)), d=4, dtype="f32", rot=4, P=1, Hq=2, Hkv=1),
+    # enough bytes for the bulk-copy form: one and several parts per token,
+    # fp32, no rotation, sequences without new tokens and rows of none
+    Paged("bulk", ((400, 390), (77, 0), (300, 220), (5, 5)), Hq=32, Hkv=4, rot=128, cap=2, spare_rows=3),
+    Paged("bulk_parts", ((350, 349), (64, 33)), Hq=64, Hkv=8, rot=64, P=24, inter=True),
+    Paged("bulk_f32", ((500, 480), (300, 211)), Hq=16, Hkv=2, d=72, rot=40, inter=True, dtype="f32", P=48, cap=1),
+    Paged("bulk_plain", ((700, 650),), Hq=24, Hkv=3, P=32),
     Paged("many", tuple((3 + b % 5, b % 3) for b in range(1500)), d=16, rot=16, P=16, Hq=1, Hkv=1),
 ]
 
@@ -87,9 +93,10 @@ def test_append_q8(c):
         np.testing.assert_array_equal(g[name].double().cpu().numpy(), want, err_msg=name)
 
 
-def test_columns_of_one_projection():
+@pytest.mark.parametrize("seqs", [((40, 9), (25, 25)), ((2500, 2400), (1500, 1000))], ids=["few", "bulk"])
+def test_columns_of_one_projection(seqs):
     """q, k and v as column blocks of one matrix (a token stride, dense heads)."""
-    c = Paged("cols", ((40, 9), (25, 25)), Hq=8, Hkv=2, d=64, rot=64)
+    c = Paged("cols", seqs, Hq=8, Hkv=2, d=64, rot=64)
     x = make(c, dev="cuda")
     whole = torch.cat([x["q"].flatten(1), x["k"].flatten(1), x["v"].flatten(1)], 1)
     q, k, v = whole[:, :512].view(-1, 8, 64), whole[:, 512:640].view(-1, 2, 64), whole[:, 640:].view(-1, 2, 64)
@@ -179,6 +186,38 @@ def test_bad_positions_and_pages_are_left_out(q8):
     pairs = [(fill, qo), (g["kd"], kd), (g["vd"], vd)] + ([] if q8 else [(g["k_pages"], kp), (g["v_pages"], vp)])
     for got, w in pairs:
         assert torch.equal(bits(got.cpu()), bits(torch.from_numpy(w).to(torch.bfloat16)))
+
+
+def test_without_queries():
+    """q left out: keys and values only, in both forms."""
+    for seqs in (((40, 9),), ((2500, 2400), (1500, 1000))):
+        c = Paged("kv", seqs, Hq=8, Hkv=8, d=128, rot=128)
+        x = make(c, dev="cuda")
+        res = []
+        for q in (x["q"], None):
+            kp, vp = x["k_pages"].clone(), x["v_pages"].clone()
+            qo = moda.moda_paged_append(q, x["k"], x["v"], kp, vp, x["table"], x["cu_q"], x["ctx"], rope=x["rope"])
+            assert (qo is None) == (q is None)
+            res.append([bits(kp), bits(vp)])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(*res))
+        assert moda.moda_device_status() == 0
+
+
+def test_expired_wait_is_reported():
+    """The bulk form's waits are bounded: with a cap of one poll some expire,
+    the call's kernels end and the status word says so."""
+    c = Paged("bulk", ((3000, 2900),), Hq=32, Hkv=4, rot=128)
+    x = make(c, dev="cuda")
+    torch.cuda.synchronize()
+    moda.moda_debug_set_wait_limit(1)
+    try:
+        moda.moda_paged_append(x["q"], x["k"], x["v"], x["k_pages"], x["v_pages"], x["table"], x["cu_q"], x["ctx"],
+                               rope=x["rope"])
+        assert moda.moda_device_status() == 6
+    finally:
+        moda.moda_debug_set_wait_limit(0)
+    assert moda.moda_device_status() == 0
 
 
 def test_other_stream_and_graph():
