@@ -15,16 +15,19 @@
 //  * One producer warp fills a ring of 64-key K and V slots by TMA, one box of
 //    16 rows per page slice, so any page size that is a multiple of 16 works;
 //    page ids and scales are fetched 32 slices at a time, one batch ahead.
-//  * Four consumer warps. With up to 16 rows each takes its own 16 keys of a
-//    stage (own softmax state, joined at the unit's end); with 32 or 64 rows
-//    two or four of them take 16 rows each of the same keys. The products are
-//    mma.sync m16n8k16: 16 rows are all a decode step has, where a tcgen05
-//    tile would be 128 rows high, seven eighths of them padding.
+//  * The products are mma.sync m16n8k16 with the KEYS as the 16 rows (S^T = K Q^T,
+//    O^T = V^T P^T): query rows then come in eights, which is what a decode step
+//    has (G heads of a token), where a tcgen05 tile would be 128 rows high. Four
+//    consumer warps, each with its own keys of a stage and its own softmax state,
+//    joined at the unit's end; with 32 or 64 rows two or four of them take 16
+//    rows each of the same keys. Up to 8 rows three CTAs fit an SM, else two. P^T is
+//    what the second product wants as its B operand, once its 8 x 8 blocks are
+//    transposed between lanes (movmatrix).
 //  * 8-bit pages: a lane reads whole 16-byte pieces of a row and turns codes
 //    into bf16 exactly, two at a time ((0x4300 | low 7 bits) is 128 + them, and
 //    (0x4300 | sign bit) is 128 or 256, so one subtraction gives the code). The
 //    order in which a lane holds features is free in a product's contracted
-//    index (queries are laid out alike) and only permutes the output columns.
+//    index (queries are laid out alike) and only permutes the output rows.
 //    A key's scale multiplies its logit, a value's scale its P: both exact, as
 //    scales are powers of two.
 //  * Rounding: logits, P, l, O in fp32; P is rounded to bf16 as the operand of
@@ -46,9 +49,6 @@
 namespace moda {
 namespace {
 
-constexpr int kConsumers = 4;                   // consumer warps
-constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kProducer = kConsumers;
 constexpr int kSliceRows = 16;
 constexpr float kLazy = 8.f;                    // log2 units before a running max moves
 
@@ -70,31 +70,39 @@ struct DecParams {
     unsigned int wait_limit;
 };
 
-constexpr int kSeqs = 128;   // sequences whose lengths are kept in shared memory
-constexpr int kCtl = 3072;   // barriers and those
+constexpr int kSeqs = 64;    // sequences whose lengths are kept in shared memory
+constexpr int kCtl = 2048;   // barriers and those
 
-template <bool Q8, int NH, int WR>
+// NH: 64-feature halves of a row; NR: 8-row tiles of a warp; WR: warps along the
+// query rows, the others split the keys.
+template <bool Q8, int NH, int NR, int WR>
 struct Cfg {
     static constexpr int D = 64 * NH;
-    static constexpr int MR = 16 * WR;
-    static constexpr int WK = kConsumers / WR;               // warps that share a stage's keys
-    static constexpr int SL = WR;                            // slices of a stage per warp
+    static constexpr int kWarps = 4;                         // consumers
+    static constexpr int kPerSM = NR == 1 ? 3 : 2;           // CTAs
+    static constexpr int kParts = kPerSM * 148;
+    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int MR = 8 * NR * WR;
+    static constexpr int WK = kWarps / WR;                   // warps that share a stage's keys
+    static constexpr int SL = WR == 4 ? 4 : WR == 2 || Q8 ? 2 : 1;  // slices of a stage per warp
+    static constexpr int SPS = SL * WK;                      // slices of a stage
+    static constexpr int KEYS = 16 * SPS;
     static constexpr int kSeqSlice = Q8 ? 2048 : 2048 * NH;  // bytes of 16 keys
     static constexpr int kDepSlice = 2048 * NH;
-    static constexpr int kSlot = 4 * kSeqSlice;
+    static constexpr int kSlot = SPS * kSeqSlice;
     static constexpr int DS = kSlot / kDepSlice;             // depth slices per stage
-    static constexpr int NS = Q8 || NH == 1 ? 8 : 5;         // ring slots
-    static constexpr int kMerge = WK == 1 ? 0 : 2 * 16 * D * 4;
-    static constexpr int kSmem = 1024 + NS * kSlot + kMerge + kCtl;
+    static constexpr int NS = kSlot == 8192 ? 8 : kSlot == 16384 ? (kPerSM == 3 ? 4 : 5) : 3;  // ring slots
+    static constexpr int kMergeBufs = WK / 2 * WR;
+    static constexpr int kMergeFloats = 8 * NR * D;
+    static constexpr int kSmem = 1024 + NS * kSlot + kMergeBufs * kMergeFloats * 4 + kCtl;
 };
 
 struct __align__(8) DecBars {
     uint64_t full[8], empty[8];
-    float scale[8][4];   // per slot and slice: scale (1 for bf16), -1: no page
-    float ml[kConsumers][16][2];
-    long long scan[kThreads / 32];
+    float scale[8][8];   // per slot and slice: scale (1 for bf16), -1: no page
+    float ml[4][16][2];
+    long long scan[9];
     long long begin_in_seq;
-    long long total, before;
     int begin_seq;
     int abort_flag;
     SeqInfo seqs[kSeqs];
@@ -131,9 +139,24 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// 0x43004300 in a register that the compiler does not see through: with two
+// constants (w & m) | c would be two instructions.
+__device__ __forceinline__ uint32_t magic_reg() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, 0x43004300;" : "=r"(r));
+    return r;
+}
 // Two int8 codes, in bytes 0 and 2 of w, as a bf16 pair (exact).
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t w) {
-    const uint32_t y = (w & 0x007f007fu) | 0x43004300u, base = (w & 0x00800080u) | 0x43004300u;
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t w, uint32_t magic) {
+    uint32_t y, base;
+    asm("lop3.b32 %0, %1, 0x007f007f, %2, 0xea;" : "=r"(y) : "r"(w), "r"(magic));     // (w & m) | magic
+    asm("lop3.b32 %0, %1, 0x00800080, %2, 0xea;" : "=r"(base) : "r"(w), "r"(magic));
     __nv_bfloat162 a, b;
     memcpy(&a, &y, 4);
     memcpy(&b, &base, 4);
@@ -149,56 +172,58 @@ __device__ __forceinline__ uint32_t bf16_at(uint32_t slice, int r, int f) {
     return slice + (f >> 6) * 2048 + r * 128 + ((((f >> 3) & 7) ^ (r & 7)) << 4) + (f & 7) * 2;
 }
 
-// The K operand of one 16-key slice, 8 keys j at a time: S += Q K^T.
-template <int NH>
-__device__ __forceinline__ void qk_bf16(uint32_t slice, const uint32_t (&qf)[NH * 4][4], float (&s)[2][4], int lane) {
-    const int r = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
+// S^T += K Q^T of one 16-key slice: keys g, g + 8 of a lane's fragment, query
+// rows 2t, 2t + 1 of each 8-row tile.
+template <int NH, int NR>
+__device__ __forceinline__ void qk_bf16(uint32_t slice, const uint32_t (&qf)[NR][NH * 4][2], float (&s)[NR][4], int lane) {
+    const int r = lane & 15, hi = lane >> 4;
 #pragma unroll
     for (int k = 0; k < NH * 4; ++k) {
-        uint32_t b[4];
-        ldsm4(bf16_at(slice, r, 16 * k + 8 * hi), b);
-        mma_bf16(s[0], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[0], b[1]);
-        mma_bf16(s[1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[2], b[3]);
+        uint32_t a[4];
+        ldsm4(bf16_at(slice, r, 16 * k + 8 * hi), a);
+#pragma unroll
+        for (int x = 0; x < NR; ++x) mma_bf16(s[x], a[0], a[1], a[2], a[3], qf[x][k][0], qf[x][k][1]);
     }
 }
-// O += P V, output tile nt = features 8 nt .. 8 nt + 7.
-template <int NH>
-__device__ __forceinline__ void pv_bf16(uint32_t slice, const uint32_t (&pf)[4], float (&o)[NH * 8][4], int lane) {
-    const int r = (lane & 7) + (((lane >> 3) & 1) << 3), hi = lane >> 4;
+// O^T += V^T P^T: output tile m = features 16 m + g, + 8.
+template <int NH, int NR>
+__device__ __forceinline__ void pv_bf16(uint32_t slice, const uint32_t (&pf)[NR][2], float (&o)[NR][NH * 4][4], int lane) {
+    const int r = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
 #pragma unroll
-    for (int n = 0; n < NH * 4; ++n) {
-        uint32_t b[4];
-        ldsm4t(bf16_at(slice, r, 16 * n + 8 * hi), b);
-        mma_bf16(o[2 * n], pf[0], pf[1], pf[2], pf[3], b[0], b[1]);
-        mma_bf16(o[2 * n + 1], pf[0], pf[1], pf[2], pf[3], b[2], b[3]);
+    for (int m = 0; m < NH * 4; ++m) {
+        uint32_t a[4];
+        ldsm4t(bf16_at(slice, r, 16 * m + 8 * hi), a);
+#pragma unroll
+        for (int x = 0; x < NR; ++x) mma_bf16(o[x][m], a[0], a[1], a[2], a[3], pf[x][0], pf[x][1]);
     }
 }
 
 // 8-bit kernels hold features permuted: lane t of a quad owns features
-// t * D/4 .. of a key row; k-step s takes its features 4s, 4s+2 and 4s+1, 4s+3.
-// Output tile nt, column n = feature n * D/8 + nt.
-template <int NH>
-__device__ __forceinline__ void qk_q8(uint32_t slice, const uint32_t (&qf)[NH * 4][4], float (&s)[2][4], int lane) {
+// t * D/4 .. of a key; k-step s takes its features 4s, 4s+2 and 4s+1, 4s+3.
+// Output tile m, row g / g + 8 = feature g * D/8 + 2m / + 1.
+template <int NH, int NR>
+__device__ __forceinline__ void qk_q8(uint32_t slice, const uint32_t (&qf)[NR][NH * 4][2], float (&s)[NR][4], int lane,
+                                      uint32_t magic) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint32_t row = slice + (8 * j + g) * 128;
+    for (int c = 0; c < NH; ++c) {  // 16 codes = 4 k-steps
+        const uint32_t at = slice + g * 128 + (((t * NH + c) ^ g) << 4);
+        const uint4 w0 = lds128(at), w1 = lds128(at + 1024);  // keys g, g + 8
+        const uint32_t a[4] = {w0.x, w0.y, w0.z, w0.w}, b[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-        for (int c = 0; c < NH; ++c) {  // 16 codes = 4 k-steps
-            const uint4 w = lds128(row + (((t * NH + c) ^ g) << 4));
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t a0 = codes_to_bf16(a[e], magic), a1 = codes_to_bf16(b[e], magic);
+            const uint32_t a2 = codes_to_bf16(a[e] >> 8, magic), a3 = codes_to_bf16(b[e] >> 8, magic);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int k = 4 * c + e;
-                mma_bf16(s[j], qf[k][0], qf[k][1], qf[k][2], qf[k][3], codes_to_bf16(ww[e]), codes_to_bf16(ww[e] >> 8));
-            }
+            for (int x = 0; x < NR; ++x) mma_bf16(s[x], a0, a1, a2, a3, qf[x][4 * c + e][0], qf[x][4 * c + e][1]);
         }
     }
 }
-template <int NH>
-__device__ __forceinline__ void pv_q8(uint32_t slice, const uint32_t (&pf)[4], float (&o)[NH * 8][4], int lane) {
+template <int NH, int NR>
+__device__ __forceinline__ void pv_q8(uint32_t slice, const uint32_t (&pf)[NR][2], float (&o)[NR][NH * 4][4], int lane,
+                                      uint32_t magic) {
     const int g = lane >> 2, t = lane & 3;
-    uint32_t w[4][NH * 2];
+    uint32_t w[4][NH * 2];  // 8 NH codes of keys 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         const int r = 2 * t + (x & 1) + 8 * (x >> 1);
@@ -211,36 +236,39 @@ __device__ __forceinline__ void pv_q8(uint32_t slice, const uint32_t (&pf)[4], f
         }
     }
 #pragma unroll
-    for (int nt = 0; nt < NH * 8; ++nt) {
-        const uint32_t sel = 0x4400u + (uint32_t)(nt & 3) * 0x1111u;  // byte nt%4 of each row, at bytes 0 and 2
-        const uint32_t b0 = codes_to_bf16(__byte_perm(w[0][nt >> 2], w[1][nt >> 2], sel));
-        const uint32_t b1 = codes_to_bf16(__byte_perm(w[2][nt >> 2], w[3][nt >> 2], sel));
-        mma_bf16(o[nt], pf[0], pf[1], pf[2], pf[3], b0, b1);
+    for (int m = 0; m < NH * 4; ++m) {
+        const int q = m >> 1;
+        const uint32_t s0 = (m & 1) ? 0x6622u : 0x4400u, s1 = (m & 1) ? 0x7733u : 0x5511u;  // codes 2m, 2m + 1 of two keys
+        const uint32_t a0 = codes_to_bf16(__byte_perm(w[0][q], w[1][q], s0), magic);
+        const uint32_t a1 = codes_to_bf16(__byte_perm(w[0][q], w[1][q], s1), magic);
+        const uint32_t a2 = codes_to_bf16(__byte_perm(w[2][q], w[3][q], s0), magic);
+        const uint32_t a3 = codes_to_bf16(__byte_perm(w[2][q], w[3][q], s1), magic);
+#pragma unroll
+        for (int x = 0; x < NR; ++x) mma_bf16(o[x][m], a0, a1, a2, a3, pf[x][0], pf[x][1]);
     }
 }
 // bf16 depth slices in the same permuted order.
-template <int NH>
-__device__ __forceinline__ void qk_bf16_perm(uint32_t slice, const uint32_t (&qf)[NH * 4][4], float (&s)[2][4], int lane) {
+template <int NH, int NR>
+__device__ __forceinline__ void qk_bf16_perm(uint32_t slice, const uint32_t (&qf)[NR][NH * 4][2], float (&s)[NR][4], int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int c = 0; c < NH * 2; ++c) {  // 8 features = 2 k-steps
+        const uint4 w0 = lds128(bf16_at(slice, g, t * 16 * NH + 8 * c)), w1 = lds128(bf16_at(slice, g + 8, t * 16 * NH + 8 * c));
 #pragma unroll
-        for (int c = 0; c < NH * 2; ++c) {  // 8 features = 2 k-steps
-            const uint4 w = lds128(bf16_at(slice, 8 * j + g, t * 16 * NH + 8 * c));
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t l0 = e ? w0.z : w0.x, h0 = e ? w0.w : w0.y, l1 = e ? w1.z : w1.x, h1 = e ? w1.w : w1.y;
+            const uint32_t a0 = __byte_perm(l0, h0, 0x5410), a2 = __byte_perm(l0, h0, 0x7632);
+            const uint32_t a1 = __byte_perm(l1, h1, 0x5410), a3 = __byte_perm(l1, h1, 0x7632);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t lo = e ? w.z : w.x, hi = e ? w.w : w.y;
-                const int k = 2 * c + e;
-                mma_bf16(s[j], qf[k][0], qf[k][1], qf[k][2], qf[k][3], __byte_perm(lo, hi, 0x5410),
-                         __byte_perm(lo, hi, 0x7632));
-            }
+            for (int x = 0; x < NR; ++x) mma_bf16(s[x], a0, a1, a2, a3, qf[x][2 * c + e][0], qf[x][2 * c + e][1]);
         }
+    }
 }
-template <int NH>
-__device__ __forceinline__ void pv_bf16_perm(uint32_t slice, const uint32_t (&pf)[4], float (&o)[NH * 8][4], int lane) {
+template <int NH, int NR>
+__device__ __forceinline__ void pv_bf16_perm(uint32_t slice, const uint32_t (&pf)[NR][2], float (&o)[NR][NH * 4][4], int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int c = 0; c < NH; ++c) {  // 8 of the lane's 8 NH columns
+    for (int c = 0; c < NH; ++c) {  // 8 of the lane's 8 NH features
         uint32_t w[4][4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -248,18 +276,19 @@ __device__ __forceinline__ void pv_bf16_perm(uint32_t slice, const uint32_t (&pf
             w[x][0] = v.x; w[x][1] = v.y; w[x][2] = v.z; w[x][3] = v.w;
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t sel = (e & 1) ? 0x7632u : 0x5410u;
-            mma_bf16(o[8 * c + e], pf[0], pf[1], pf[2], pf[3], __byte_perm(w[0][e >> 1], w[1][e >> 1], sel),
-                     __byte_perm(w[2][e >> 1], w[3][e >> 1], sel));
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t a0 = __byte_perm(w[0][e], w[1][e], 0x5410), a1 = __byte_perm(w[0][e], w[1][e], 0x7632);
+            const uint32_t a2 = __byte_perm(w[2][e], w[3][e], 0x5410), a3 = __byte_perm(w[2][e], w[3][e], 0x7632);
+#pragma unroll
+            for (int x = 0; x < NR; ++x) mma_bf16(o[x][4 * c + e], a0, a1, a2, a3, pf[x][0], pf[x][1]);
         }
     }
 }
 
-// Feature of element (nt, c) of a lane's output fragment.
+// Feature of row g (hi = 0) or g + 8 (hi = 1) of output tile m.
 template <bool Q8, int NH>
-__device__ __forceinline__ int out_col(int nt, int c, int t) {
-    return Q8 ? (2 * t + c) * (8 * NH) + nt : 8 * nt + 2 * t + c;
+__device__ __forceinline__ int out_col(int m, int hi, int g) {
+    return Q8 ? g * (8 * NH) + 2 * m + hi : 16 * m + g + 8 * hi;
 }
 
 // Keys of a bf16 slice with a non-finite value, as a 16-bit mask.
@@ -283,27 +312,34 @@ __device__ __forceinline__ uint32_t nonfinite_keys(uint32_t slice, int lane) {
 }
 
 // Adds P V of the keys in `bad` to the rows whose P is not 0.
-template <bool Q8, int NH>
-__device__ __forceinline__ void add_nonfinite(uint32_t slice, uint32_t bad, const float (&p)[2][4], float (&o)[NH * 8][4],
+template <bool Q8, int NH, int NR>
+__device__ __forceinline__ void add_nonfinite(uint32_t slice, uint32_t bad, const float (&p)[NR][4], float (&o)[NR][NH * 4][4],
                                               int lane) {
+    const int g = lane >> 2, t = lane & 3;
     for (; bad; bad &= bad - 1) {
-        const int k = __ffs(bad) - 1, src = (lane & ~3) | ((k & 7) >> 1);
-        float pr[2];
+        const int k = __ffs(bad) - 1, src = (k & 7) * 4 + t;
+        float pr[NR][2];
+        bool any = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float a = (k & 8) ? ((k & 1) ? p[1][2 * h + 1] : p[1][2 * h]) : ((k & 1) ? p[0][2 * h + 1] : p[0][2 * h]);
-            pr[h] = __shfl_sync(0xffffffffu, a, src);
-        }
-        if (!__any_sync(0xffffffffu, pr[0] != 0.f || pr[1] != 0.f)) continue;  // what an unused row of a page held
+        for (int x = 0; x < NR; ++x)
 #pragma unroll
-        for (int nt = 0; nt < NH * 8; ++nt)
+            for (int e = 0; e < 2; ++e) {
+                pr[x][e] = __shfl_sync(0xffffffffu, (k & 8) ? p[x][2 + e] : p[x][e], src);
+                any |= pr[x][e] != 0.f;
+            }
+        if (!__any_sync(0xffffffffu, any)) continue;  // what an unused row of a page held
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+        for (int m = 0; m < NH * 4; ++m)
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
                 uint16_t raw;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(bf16_at(slice, k, out_col<Q8, NH>(nt, c, lane & 3))) : "memory");
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(raw) : "r"(bf16_at(slice, k, out_col<Q8, NH>(m, hi, g))) : "memory");
                 const float v = __uint_as_float((uint32_t)raw << 16);
-                if (pr[0] != 0.f) o[nt][c] += pr[0] * v;
-                if (pr[1] != 0.f) o[nt][2 + c] += pr[1] * v;
+#pragma unroll
+                for (int x = 0; x < NR; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (pr[x][e] != 0.f) o[x][m][2 * hi + e] += pr[x][e] * v;
             }
     }
 }
@@ -324,24 +360,25 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, uin
         : "memory");
 }
 
-template <bool Q8, int NH, int WR>
-__global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_constant__ DecParams p) {
-    using C = Cfg<Q8, NH, WR>;
+template <bool Q8, int NH, int NR, int WR>
+__global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR, WR>::kPerSM) paged_dec_kernel(const __grid_constant__ DecParams p) {
+    using C = Cfg<Q8, NH, NR, WR>;
+    constexpr int kThreads = C::kThreads;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* base = smem_raw + (ring - ptx::smem_u32(smem_raw));
     float* merge = reinterpret_cast<float*>(base + C::NS * C::kSlot);
-    DecBars* bars = reinterpret_cast<DecBars*>(base + C::NS * C::kSlot + C::kMerge);
+    DecBars* bars = reinterpret_cast<DecBars*>(base + C::NS * C::kSlot + C::kMergeBufs * C::kMergeFloats * 4);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const PagedCache& c = p.c;
-    const long long max_keys = min((long long)c.max_blocks * c.page_size, 0x7fffffc0LL);
+    const long long max_keys = min((long long)c.max_blocks * c.page_size, 0x7fffff00LL);
     const int cta = blockIdx.x;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NS; ++s) {
             ptx::mbar_init(&bars->full[s], 1);
-            ptx::mbar_init(&bars->empty[s], kConsumers);
+            ptx::mbar_init(&bars->empty[s], C::kWarps);
         }
         bars->abort_flag = 0;
         ptx::fence_barrier_init();
@@ -355,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
     for (int b = b0; b < b1; ++b) {
         const SeqInfo s = seq_info(c, b);
         if (b < kSeqs) bars->seqs[b] = s;
-        mine += seq_stages<C::MR>(s, p.G, p.DSL, C::DS, max_keys);
+        mine += seq_stages<C::MR, C::KEYS>(s, p.G, p.DSL, C::DS, max_keys);
     }
     auto seq_at = [&](int b) { return b < kSeqs ? bars->seqs[b] : seq_info(c, b); };
     long long incl = mine * c.Hkv;
@@ -381,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
         long long at = incl - mine * c.Hkv;
         if (lo >= at && lo < incl) {  // one thread: the CTA's part begins in its run
             for (int b = b0; b < b1; ++b) {
-                const long long n = seq_stages<C::MR>(seq_at(b), p.G, p.DSL, C::DS, max_keys) * c.Hkv;
+                const long long n = seq_stages<C::MR, C::KEYS>(seq_at(b), p.G, p.DSL, C::DS, max_keys) * c.Hkv;
                 if (lo < at + n) {
                     bars->begin_seq = b;
                     bars->begin_in_seq = lo - at;
@@ -405,11 +442,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
     int first;                      // first stage of the current unit's piece
     {
         long long in = bars->begin_in_seq;
-        const long long n = seq_stages<C::MR>(sq, p.G, p.DSL, C::DS, max_keys);
+        const long long n = seq_stages<C::MR, C::KEYS>(sq, p.G, p.DSL, C::DS, max_keys);
         kvh = (int)(in / n);
         in -= (long long)kvh * n;
         for (;; ++rt) {
-            const int st = unit_shape<C::MR>(sq, rt, p.G, p.DSL, C::DS, max_keys).st;
+            const int st = unit_shape<C::MR, C::KEYS>(sq, rt, p.G, p.DSL, C::DS, max_keys).st;
             if (in < st) break;
             in -= st;
         }
@@ -427,20 +464,20 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
     };
 
     if (!p.split && first > 0) {  // the unit belongs to the CTA it starts in
-        left -= unit_shape<C::MR>(sq, rt, p.G, p.DSL, C::DS, max_keys).st - first;
+        left -= unit_shape<C::MR, C::KEYS>(sq, rt, p.G, p.DSL, C::DS, max_keys).st - first;
         if (left > 0) next_unit();
     }
 
-    if (warp == kProducer) {
+    if (warp == C::kWarps) {
         int slot = 0, ph = 1, issued = 0;
         bool ok = true;
         while (left > 0) {
-            const UnitShape u = unit_shape<C::MR>(sq, rt, p.G, p.DSL, C::DS, max_keys);
+            const UnitShape u = unit_shape<C::MR, C::KEYS>(sq, rt, p.G, p.DSL, C::DS, max_keys);
             const int end = p.split ? (int)min((long long)u.st, first + left) : u.st;
-            // page slices [4 first, ...) of the unit, 32 at a time: lane l
+            // page slices [SPS first, ...) of the unit, 32 at a time: lane l
             // holds slice 32 batch + l of the piece; the next batch's page ids
             // are in flight while this one's boxes are issued
-            const int sl0 = first * 4, sl_all = u.st_seq * 4;
+            const int sl0 = first * C::SPS, sl_all = u.st_seq * C::SPS;
             auto fetch = [&](int sl) {  // page of slice sl, num_pages: none
                 const int key = sl * kSliceRows;
                 int pg = -1;
@@ -460,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
             scales(page, ks, vs);
             for (int st = first; st < end; ++st) {
                 const bool seq = st < u.st_seq;
-                const int rel = st * 4 - sl0;
+                const int rel = st * C::SPS - sl0;
                 if (seq && rel && (rel & 31) == 0) {
                     page = page_next;
                     ks = ks_next;
@@ -480,16 +517,16 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
                         if (seq) {
                             const int per_slice = Q8 ? 1 : NH;
                             const int sl = lane / per_slice, half = lane % per_slice;
-                            const int src = (rel & 31) + (sl & 3);
+                            const int src = (rel & 31) + (sl & (C::SPS - 1));
                             const int pg = __shfl_sync(0xffffffffu, page, src);
                             const float sc = __shfl_sync(0xffffffffu, kv ? vs : ks, src);
                             const float none = __shfl_sync(0xffffffffu, ks, src);
-                            if (lane < 4 * per_slice && half == 0) bars->scale[slot][sl] = none < 0.f ? -1.f : sc;
+                            if (lane < C::SPS * per_slice && half == 0) bars->scale[slot][sl] = none < 0.f ? -1.f : sc;
                             __syncwarp();
                             if (lane == 0) ptx::mbar_arrive_expect_tx(bar, C::kSlot);
                             __syncwarp();
-                            if (lane < 4 * per_slice) {
-                                const int key = (st * 4 + sl) * kSliceRows;
+                            if (lane < C::SPS * per_slice) {
+                                const int key = (st * C::SPS + sl) * kSliceRows;
                                 // a page that is not there lies outside the map: zeros
                                 load_box(dst + sl * C::kSeqSlice + half * 2048, kv ? &p.tm_v : &p.tm_k, bar, half * 64,
                                          pg < 0 ? 0 : key % c.page_size, kvh, pg < 0 ? c.num_pages : pg);
@@ -524,51 +561,62 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
     }
 
     // ------------------------------------------------------ consumer warps
-    const int wr = warp / C::WK, wk = warp % C::WK;  // rows 16 wr .., keys of slices wk, wk + WK, ..
+    const int wr = warp / C::WK, wk = warp % C::WK;  // rows 8 NR wr .., keys of slices wk, wk + WK, ..
     const int g = lane >> 2, t = lane & 3;
+    const uint32_t magic = magic_reg();
     int slot = 0, ph = 0;
     bool ok = true;
     while (left > 0) {
-        const UnitShape u = unit_shape<C::MR>(sq, rt, p.G, p.DSL, C::DS, max_keys);
+        const UnitShape u = unit_shape<C::MR, C::KEYS>(sq, rt, p.G, p.DSL, C::DS, max_keys);
         const int end = p.split ? (int)min((long long)u.st, first + left) : u.st;
-        // this lane's rows g and g + 8 of the warp's 16
-        int tok[2], pos[2];
-        uint32_t qf[NH * 4][4];
+        const int row0 = u.r0 + 8 * NR * wr, rows = u.rows - 8 * NR * wr;  // this warp's rows (rows may be <= 0)
+        auto out_row = [&](int r) {  // packed row and head of row r of the sequence
+            return (long long)(sq.q0 + r / p.G) * p.Hq + kvh * p.G + r % p.G;
+        };
+        // queries of row g of each tile, and token and position of rows 2t, 2t + 1
+        uint32_t qf[NR][NH * 4][2];
+        int tok[NR][2], pos[NR][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = u.r0 + 16 * wr + g + 8 * h;
-            const bool in = r < u.r0 + u.rows;
-            tok[h] = in ? r / p.G : -1;
-            pos[h] = in ? sq.pos0 + tok[h] : -1;
-            const __nv_bfloat16* row =
-                p.q + ((long long)(sq.q0 + max(tok[h], 0)) * p.Hq + kvh * p.G + (in ? r % p.G : 0)) * c.d;
+        for (int x = 0; x < NR; ++x) {
+            const bool in = 8 * x + g < rows;
+            const __nv_bfloat16* row = p.q + (in ? out_row(row0 + 8 * x + g) : 0) * c.d;
 #pragma unroll
             for (int k = 0; k < NH * 4; ++k) {
                 if (Q8) {
                     const int f = t * 16 * NH + 4 * k;  // features f .. f+3
                     uint2 w = make_uint2(0, 0);
                     if (in && f < c.d) w = *reinterpret_cast<const uint2*>(row + f);
-                    qf[k][h] = __byte_perm(w.x, w.y, 0x5410);
-                    qf[k][2 + h] = __byte_perm(w.x, w.y, 0x7632);
+                    qf[x][k][0] = __byte_perm(w.x, w.y, 0x5410);
+                    qf[x][k][1] = __byte_perm(w.x, w.y, 0x7632);
                 } else {
                     const int f = 16 * k + 2 * t;
-                    qf[k][h] = in && f < c.d ? *reinterpret_cast<const uint32_t*>(row + f) : 0u;
-                    qf[k][2 + h] = in && f + 8 < c.d ? *reinterpret_cast<const uint32_t*>(row + f + 8) : 0u;
+                    qf[x][k][0] = in && f < c.d ? *reinterpret_cast<const uint32_t*>(row + f) : 0u;
+                    qf[x][k][1] = in && f + 8 < c.d ? *reinterpret_cast<const uint32_t*>(row + f + 8) : 0u;
                 }
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * x + 2 * t + e;
+                tok[x][e] = r < rows ? (row0 + r) / p.G : -1;
+                pos[x][e] = r < rows ? sq.pos0 + tok[x][e] : -1;
+            }
         }
-        float o[NH * 8][4];
+        float o[NR][NH * 4][4];
+        float m[NR][2], l[NR][2];
 #pragma unroll
-        for (int n = 0; n < NH * 8; ++n)
+        for (int x = 0; x < NR; ++x) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            for (int n = 0; n < NH * 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x][n][e] = 0.f;
+            m[x][0] = m[x][1] = -INFINITY;
+            l[x][0] = l[x][1] = 0.f;
+        }
 
         const int pos_first = sq.pos0 + u.tok0;  // keys up to here are seen by every row of the tile
         for (int st = first; st < end; ++st) {
             const bool seq = st < u.st_seq;
-            const int kslot = slot;
-            int kph = ph;
+            const int kslot = slot, kph = ph;
             if (++slot == C::NS) { slot = 0; ph ^= 1; }
             const int vslot = slot, vph = ph;
             if (++slot == C::NS) { slot = 0; ph ^= 1; }
@@ -577,92 +625,99 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
                 ok = false;
             }
             const uint32_t ka = ring + kslot * C::kSlot, va = ring + vslot * C::kSlot;
-            float s[C::SL][2][4];
-            bool some = !seq || st * 64 + 63 > pos_first;  // some row is masked somewhere in the stage
-            bool part[C::SL];                              // this warp's slice i takes part
+            const uint32_t bytes = seq ? C::kSeqSlice : C::kDepSlice;
+            float s[C::SL][NR][4];
+            const bool some = !seq || st * C::KEYS + C::KEYS - 1 > pos_first;  // some row is masked somewhere in the stage
+            bool part[C::SL];                                                // this warp's slice i takes part
 #pragma unroll
             for (int i = 0; i < C::SL; ++i) {
                 const int sl = wk + i * C::WK;
                 part[i] = seq || sl < C::DS;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int x = 0; x < NR; ++x)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][j][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) s[i][x][e] = 0.f;
                 float ksc = 1.f;
                 if (ok && part[i]) {
                     if (seq) {
                         ksc = bars->scale[kslot][sl];
-                        if (Q8) qk_q8<NH>(ka + sl * C::kSeqSlice, qf, s[i], lane);
-                        else qk_bf16<NH>(ka + sl * C::kSeqSlice, qf, s[i], lane);
+                        if (Q8) qk_q8<NH, NR>(ka + sl * bytes, qf, s[i], lane, magic);
+                        else qk_bf16<NH, NR>(ka + sl * bytes, qf, s[i], lane);
                     } else {
-                        if (Q8) qk_bf16_perm<NH>(ka + sl * C::kDepSlice, qf, s[i], lane);
-                        else qk_bf16<NH>(ka + sl * C::kDepSlice, qf, s[i], lane);
+                        if (Q8) qk_bf16_perm<NH, NR>(ka + sl * bytes, qf, s[i], lane);
+                        else qk_bf16<NH, NR>(ka + sl * bytes, qf, s[i], lane);
                     }
                 }
                 const float mul = p.sl2 * (Q8 ? ksc : 1.f);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int x = 0; x < NR; ++x)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][j][e] *= mul;
-                const int x = (st - u.st_seq) * C::DS + sl;
+                    for (int e = 0; e < 4; ++e) s[i][x][e] *= mul;
                 if (!part[i]) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int x = 0; x < NR; ++x)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) s[i][j][e] = -INFINITY;
+                        for (int e = 0; e < 4; ++e) s[i][x][e] = -INFINITY;
                 } else if (some || ksc < 0.f) {
-                    const int key0 = (st * 4 + sl) * kSliceRows;
-                    const int dtok = seq || !p.DSL ? 0 : u.tok0 + x / p.DSL, dsl = seq || !p.DSL ? 0 : x % p.DSL * kSliceRows;
+                    const int key0 = (st * C::SPS + sl) * kSliceRows;
+                    const int dx = (st - u.st_seq) * C::DS + sl;
+                    const int dtok = seq || !p.DSL ? 0 : u.tok0 + dx / p.DSL, dsl = seq || !p.DSL ? 0 : dx % p.DSL * kSliceRows;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int x = 0; x < NR; ++x)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int k = 8 * j + 2 * t + (e & 1), h = e >> 1;
-                            const bool see = seq ? key0 + k <= pos[h] && key0 + k < u.nk && ksc >= 0.f
-                                                 : tok[h] == dtok && dsl + k < p.Ld;
-                            if (!see) s[i][j][e] = -INFINITY;
+                            const int k = g + 8 * (e >> 1), r = e & 1;
+                            const bool see = seq ? key0 + k <= pos[x][r] && key0 + k < u.nk && ksc >= 0.f
+                                                 : tok[x][r] == dtok && dsl + k < p.Ld;
+                            if (!see) s[i][x][e] = -INFINITY;
                         }
                 }
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bars->empty[kslot]);
             // ---- online softmax over this warp's keys of the stage
-            float mx[2] = {-INFINITY, -INFINITY};
+            float mx[NR][2];
+            bool moves = false;
 #pragma unroll
-            for (int i = 0; i < C::SL; ++i)
+            for (int x = 0; x < NR; ++x)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int e = 0; e < 2; ++e) {
+                    float v = fmaxf(s[0][x][e], s[0][x][2 + e]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[i][j][e]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-            }
-            if (__any_sync(0xffffffffu, mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy)) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float mn = fmaxf(m[h], mx[h]);
-                    const float corr = mn == -INFINITY ? 1.f : ptx::ex2(m[h] - mn);
-                    l[h] *= corr;
-                    m[h] = mn;
-#pragma unroll
-                    for (int n = 0; n < NH * 8; ++n) {
-                        o[n][2 * h] *= corr;
-                        o[n][2 * h + 1] *= corr;
-                    }
+                    for (int i = 1; i < C::SL; ++i) v = fmaxf(v, fmaxf(s[i][x][e], s[i][x][2 + e]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    mx[x][e] = v;
+                    moves |= v > m[x][e] + kLazy;
                 }
+            if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+                for (int x = 0; x < NR; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mn = fmaxf(m[x][e], mx[x][e]);
+                        const float corr = mn == -INFINITY ? 1.f : ptx::ex2(m[x][e] - mn);
+                        l[x][e] *= corr;
+                        m[x][e] = mn;
+#pragma unroll
+                        for (int n = 0; n < NH * 4; ++n) {
+                            o[x][n][e] *= corr;
+                            o[x][n][2 + e] *= corr;
+                        }
+                    }
             }
-            const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-            for (int i = 0; i < C::SL; ++i)
+            for (int x = 0; x < NR; ++x) {
+                const float ref[2] = {m[x][0] == -INFINITY ? 0.f : m[x][0], m[x][1] == -INFINITY ? 0.f : m[x][1]};
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int i = 0; i < C::SL; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[i][j][e] = ptx::ex2(s[i][j][e] - ref[e >> 1]);
-                        l[e >> 1] += s[i][j][e];
+                        s[i][x][e] = ptx::ex2(s[i][x][e] - ref[e & 1]);
+                        l[x][e & 1] += s[i][x][e];
                     }
+            }
             if (ok && !__all_sync(0xffffffffu, ptx::mbar_wait(&bars->full[vslot], vph, p.wait_limit, abort_flag))) {
                 if (lane == 0) fail();
                 ok = false;
@@ -672,20 +727,19 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
                 uint32_t bad[C::SL];
 #pragma unroll
                 for (int i = 0; i < C::SL; ++i) {
-                    const uint32_t sl = va + (wk + i * C::WK) * (seq ? C::kSeqSlice : C::kDepSlice);
                     bad[i] = 0;
                     if (ok && part[i]) {
-                        bad[i] = nonfinite_keys<NH>(sl, lane);
-                        if (bad[i]) add_nonfinite<Q8, NH>(sl, bad[i], s[i], o, lane);
+                        bad[i] = nonfinite_keys<NH>(va + (wk + i * C::WK) * bytes, lane);
+                        if (bad[i]) add_nonfinite<Q8, NH, NR>(va + (wk + i * C::WK) * bytes, bad[i], s[i], o, lane);
                     }
                 }
                 // warps that share the keys have all read them before they are cleared
-                if (WR > 1) ptx::bar_sync(2, kConsumers * 32); else __syncwarp();
+                if (WR > 1) ptx::bar_sync(2, C::kWarps * 32); else __syncwarp();
 #pragma unroll
                 for (int i = 0; i < C::SL; ++i)
-                    if (bad[i]) clear_keys<NH>(va + (wk + i * C::WK) * (seq ? C::kSeqSlice : C::kDepSlice), bad[i], lane);
+                    if (bad[i]) clear_keys<NH>(va + (wk + i * C::WK) * bytes, bad[i], lane);
                 ptx::fence_proxy_async_smem();  // before the slot's next copy
-                if (WR > 1) ptx::bar_sync(2, kConsumers * 32); else __syncwarp();
+                if (WR > 1) ptx::bar_sync(2, C::kWarps * 32); else __syncwarp();
             }
 #pragma unroll
             for (int i = 0; i < C::SL; ++i) {
@@ -693,124 +747,147 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
                 if (!ok || !part[i]) continue;
                 float vsc = 1.f;
                 if (Q8 && seq) vsc = fmaxf(bars->scale[vslot][sl], 0.f);
-                uint32_t pf[4];
-                pf[0] = ptx::pack_bf16x2(s[i][0][0] * vsc, s[i][0][1] * vsc);
-                pf[1] = ptx::pack_bf16x2(s[i][0][2] * vsc, s[i][0][3] * vsc);
-                pf[2] = ptx::pack_bf16x2(s[i][1][0] * vsc, s[i][1][1] * vsc);
-                pf[3] = ptx::pack_bf16x2(s[i][1][2] * vsc, s[i][1][3] * vsc);
+                uint32_t pf[NR][2];
+#pragma unroll
+                for (int x = 0; x < NR; ++x)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        pf[x][h] = transpose8x8(Q8 ? ptx::pack_bf16x2(s[i][x][2 * h] * vsc, s[i][x][2 * h + 1] * vsc)
+                                                   : ptx::pack_bf16x2(s[i][x][2 * h], s[i][x][2 * h + 1]));
                 if (seq) {
-                    if (Q8) pv_q8<NH>(va + sl * C::kSeqSlice, pf, o, lane);
-                    else pv_bf16<NH>(va + sl * C::kSeqSlice, pf, o, lane);
+                    if (Q8) pv_q8<NH, NR>(va + sl * bytes, pf, o, lane, magic);
+                    else pv_bf16<NH, NR>(va + sl * bytes, pf, o, lane);
                 } else {
-                    if (Q8) pv_bf16_perm<NH>(va + sl * C::kDepSlice, pf, o, lane);
-                    else pv_bf16<NH>(va + sl * C::kDepSlice, pf, o, lane);
+                    if (Q8) pv_bf16_perm<NH, NR>(va + sl * bytes, pf, o, lane);
+                    else pv_bf16<NH, NR>(va + sl * bytes, pf, o, lane);
                 }
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bars->empty[vslot]);
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        }
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int sh = 4; sh < 32; sh *= 2) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], sh);
         // ---- join the warps that shared the rows: upper half into lower half
         if (C::WK > 1) {
 #pragma unroll
             for (int half = C::WK / 2; half >= 1; half /= 2) {
-                ptx::bar_sync(1, kConsumers * 32);  // the buffers are free
-                const int buf = wr * (C::WK / 2 > 1 ? C::WK / 2 : 1) + wk % half;
-                float* mo = merge + buf * 16 * C::D;
+                ptx::bar_sync(1, C::kWarps * 32);  // the buffers are free
+                const int buf = wr * (C::WK / 2) + wk % half;
+                float* mo = merge + buf * C::kMergeFloats;
                 if (wk >= half && wk < 2 * half) {
 #pragma unroll
-                    for (int n = 0; n < NH * 8; ++n)
+                    for (int x = 0; x < NR; ++x) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) mo[(n * 4 + e) * 32 + lane] = o[n][e];
-                    if (t == 0) {
+                        for (int n = 0; n < NH * 4; ++n)
+                            *reinterpret_cast<float4*>(mo + ((x * NH * 4 + n) * 32 + lane) * 4) =
+                                make_float4(o[x][n][0], o[x][n][1], o[x][n][2], o[x][n][3]);
+                        if (g == 0) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            bars->ml[buf][g + 8 * h][0] = m[h];
-                            bars->ml[buf][g + 8 * h][1] = l[h];
+                            for (int e = 0; e < 2; ++e) {
+                                bars->ml[buf][8 * x + 2 * t + e][0] = m[x][e];
+                                bars->ml[buf][8 * x + 2 * t + e][1] = l[x][e];
+                            }
                         }
                     }
                 }
-                ptx::bar_sync(1, kConsumers * 32);
+                ptx::bar_sync(1, C::kWarps * 32);
                 if (wk < half) {
-                    float c1[2], c2[2];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float m2 = bars->ml[buf][g + 8 * h][0], l2 = bars->ml[buf][g + 8 * h][1];
-                        const float mn = fmaxf(m[h], m2), rf = mn == -INFINITY ? 0.f : mn;
-                        c1[h] = ptx::ex2(m[h] - rf);
-                        c2[h] = ptx::ex2(m2 - rf);
-                        l[h] = l[h] * c1[h] + l2 * c2[h];
-                        m[h] = mn;
+                    for (int x = 0; x < NR; ++x) {
+                        float c1[2], c2[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float m2 = bars->ml[buf][8 * x + 2 * t + e][0], l2 = bars->ml[buf][8 * x + 2 * t + e][1];
+                            const float mn = fmaxf(m[x][e], m2), rf = mn == -INFINITY ? 0.f : mn;
+                            c1[e] = ptx::ex2(m[x][e] - rf);
+                            c2[e] = ptx::ex2(m2 - rf);
+                            l[x][e] = l[x][e] * c1[e] + l2 * c2[e];
+                            m[x][e] = mn;
+                        }
+#pragma unroll
+                        for (int n = 0; n < NH * 4; ++n) {
+                            const float4 v = *reinterpret_cast<const float4*>(mo + ((x * NH * 4 + n) * 32 + lane) * 4);
+                            o[x][n][0] = o[x][n][0] * c1[0] + v.x * c2[0];
+                            o[x][n][1] = o[x][n][1] * c1[1] + v.y * c2[1];
+                            o[x][n][2] = o[x][n][2] * c1[0] + v.z * c2[0];
+                            o[x][n][3] = o[x][n][3] * c1[1] + v.w * c2[1];
+                        }
                     }
-#pragma unroll
-                    for (int n = 0; n < NH * 8; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[n][e] = o[n][e] * c1[e >> 1] + mo[(n * 4 + e) * 32 + lane] * c2[e >> 1];
                 }
             }
         }
         const bool whole = first == 0 && end == u.st;
-        if (wk == 0) {
-            if (whole) {
+        if (wk == 0 && whole) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (tok[h] < 0) continue;
-                    const int r = u.r0 + 16 * wr + g + 8 * h;
-                    const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
-                    const long long row = (long long)(sq.q0 + tok[h]) * p.Hq + kvh * p.G + r % p.G;
-                    __nv_bfloat16* dst = p.out + row * c.d;
-                    if (Q8) {
+            for (int x = 0; x < NR; ++x) {
+                float inv[2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int f0 = out_col<true, NH>(0, e, t);
+                for (int e = 0; e < 2; ++e) inv[e] = l[x][e] == 0.f ? 0.f : 1.f / l[x][e];
+                if (Q8) {  // 8 NH consecutive features of rows 2t, 2t + 1
 #pragma unroll
-                            for (int n = 0; n < NH * 8; n += 8)
-                                if (f0 + n < c.d)
-                                    *reinterpret_cast<uint4*>(dst + f0 + n) =
-                                        make_uint4(ptx::pack_bf16x2(o[n][2 * h + e] * inv, o[n + 1][2 * h + e] * inv),
-                                                   ptx::pack_bf16x2(o[n + 2][2 * h + e] * inv, o[n + 3][2 * h + e] * inv),
-                                                   ptx::pack_bf16x2(o[n + 4][2 * h + e] * inv, o[n + 5][2 * h + e] * inv),
-                                                   ptx::pack_bf16x2(o[n + 6][2 * h + e] * inv, o[n + 7][2 * h + e] * inv));
-                        }
-                    } else {
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = 8 * x + 2 * t + e, f0 = g * 8 * NH;
+                        if (r >= rows) continue;
+                        __nv_bfloat16* dst = p.out + out_row(row0 + r) * c.d + f0;
 #pragma unroll
-                        for (int n = 0; n < NH * 8; ++n)
-                            if (8 * n + 2 * t < c.d)
-                                *reinterpret_cast<uint32_t*>(dst + 8 * n + 2 * t) =
-                                    ptx::pack_bf16x2(o[n][2 * h] * inv, o[n][2 * h + 1] * inv);
+                        for (int n = 0; n < NH * 4; n += 4)
+                            if (f0 + 2 * n < c.d)
+                                *reinterpret_cast<uint4*>(dst + 2 * n) =
+                                    make_uint4(ptx::pack_bf16x2(o[x][n][e] * inv[e], o[x][n][2 + e] * inv[e]),
+                                               ptx::pack_bf16x2(o[x][n + 1][e] * inv[e], o[x][n + 1][2 + e] * inv[e]),
+                                               ptx::pack_bf16x2(o[x][n + 2][e] * inv[e], o[x][n + 2][2 + e] * inv[e]),
+                                               ptx::pack_bf16x2(o[x][n + 3][e] * inv[e], o[x][n + 3][2 + e] * inv[e]));
                     }
-                    if (t == 0 && p.lse) p.lse[row] = l[h] == 0.f ? -INFINITY : (m[h] + __log2f(l[h])) * 0.6931471805599453f;
+                } else {  // 8 x 8 blocks (feature, row) transposed: features 2t, 2t + 1 of row g
+                    const bool in = 8 * x + g < rows;
+                    __nv_bfloat16* dst = p.out + (in ? out_row(row0 + 8 * x + g) : 0) * c.d;
+#pragma unroll
+                    for (int n = 0; n < NH * 4; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t w = transpose8x8(ptx::pack_bf16x2(o[x][n][2 * h] * inv[0], o[x][n][2 * h + 1] * inv[1]));
+                            const int f = 16 * n + 8 * h + 2 * t;
+                            if (in && f < c.d) *reinterpret_cast<uint32_t*>(dst + f) = w;
+                        }
                 }
-            } else {
-                // a part: the one that starts the unit goes to slot 2 cta + 1
-                const int ps = 2 * cta + (first == 0 ? 1 : 0);
-                float* po = p.part_o + ((long long)ps * C::MR + 16 * wr) * C::D;
-                float* pm = p.part_ml + ((long long)ps * C::MR + 16 * wr) * 2;
+                if (g == 0 && p.lse)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (tok[h] < 0) continue;
-                    const int r = g + 8 * h;
+                    for (int e = 0; e < 2; ++e)
+                        if (8 * x + 2 * t + e < rows)
+                            p.lse[out_row(row0 + 8 * x + 2 * t + e)] =
+                                l[x][e] == 0.f ? -INFINITY : (m[x][e] + __log2f(l[x][e])) * 0.6931471805599453f;
+            }
+        } else if (wk == 0) {
+            // a part: the one that starts the unit goes to slot 2 cta + 1
+            const int ps = 2 * cta + (first == 0 ? 1 : 0);
+            const long long pr = (long long)ps * C::MR + 8 * NR * wr;
 #pragma unroll
-                    for (int n = 0; n < NH * 8; ++n) {
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * x + 2 * t + e;
+                    if (r >= rows) continue;
+                    float* po = p.part_o + (pr + r) * C::D;
+#pragma unroll
+                    for (int n = 0; n < NH * 4; ++n) {
                         if (Q8) {
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) po[r * C::D + out_col<true, NH>(n, e, t)] = o[n][2 * h + e];
+                            *reinterpret_cast<float2*>(po + out_col<true, NH>(n, 0, g)) = make_float2(o[x][n][e], o[x][n][2 + e]);
                         } else {
-                            *reinterpret_cast<float2*>(po + r * C::D + 8 * n + 2 * t) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
+                            po[out_col<false, NH>(n, 0, g)] = o[x][n][e];
+                            po[out_col<false, NH>(n, 1, g)] = o[x][n][2 + e];
                         }
                     }
-                    if (t == 0) *reinterpret_cast<float2*>(pm + r * 2) = make_float2(m[h], l[h]);
+                    if (g == 0) *reinterpret_cast<float2*>(p.part_ml + (pr + r) * 2) = make_float2(m[x][e], l[x][e]);
                 }
-                if (first == 0 && warp == 0 && lane == 0) {
-                    // parts up to the one that holds the unit's last stage
-                    const long long last = hi - left + u.st - 1;  // its index in the list (this piece starts at hi - left)
-                    const int c_last = (int)(((last + 1) * W + total - 1) / total) - 1;
-                    p.desc[cta] = make_int4(b, kvh, rt, (c_last - cta + 1) | u.rows << 16);
-                }
+            if (first == 0 && warp == 0 && lane == 0) {
+                // parts up to the one that holds the unit's last stage
+                const long long last = hi - left + u.st - 1;  // its index in the list (this piece starts at hi - left)
+                const int c_last = (int)(((last + 1) * W + total - 1) / total) - 1;
+                p.desc[cta] = make_int4(b, kvh, rt, (c_last - cta + 1) | u.rows << 16);
             }
         }
         left -= end - first;
@@ -818,13 +895,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_dec_kernel(const __grid_con
     }
 }
 
-constexpr int kParts = 2 * 148;   // two CTAs per SM
 constexpr int kWholeKeys = 512;
 constexpr int kMinStages = 1;
 
-int rows_class(int max_q, int G) {
+// Query rows of a unit by the rows a sequence has: 8, 16, 32 or 64.
+int rows_of(int max_q, int G) {
     const long long r = (long long)max_q * G;
-    return r <= 16 ? 1 : r <= 32 ? 2 : 4;
+    return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : 64;
 }
 
 bool encode(CUtensorMap* m, bool u8, const void* base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
@@ -837,9 +914,9 @@ bool encode(CUtensorMap* m, bool u8, const void* base, const cuuint64_t (&dims)[
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool Q8, int NH, int WR>
+template <bool Q8, int NH, int NR, int WR>
 cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
-    using C = Cfg<Q8, NH, WR>;
+    using C = Cfg<Q8, NH, NR, WR>;
     DecParams p;
     memset(&p, 0, sizeof(p));
     const PagedCache& c = a.c;
@@ -869,7 +946,7 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.lse = a.lse;
     p.Hq = a.Hq; p.G = a.G; p.Ld = a.Ld; p.DSL = (a.Ld + kSliceRows - 1) / kSliceRows;
-    p.W = kParts;
+    p.W = C::kParts;
     p.min_stages = kMinStages;
     // the longest unit the block table allows, in stages: short ones stay whole
     // and save the join
@@ -879,25 +956,26 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
     p.wait_limit = a.wait_limit;
     char* ws = static_cast<char*>(a.workspace);
     p.desc = reinterpret_cast<int4*>(ws);
-    p.part_ml = reinterpret_cast<float*>(ws + kParts * sizeof(int4));
-    p.part_o = p.part_ml + (size_t)2 * kParts * C::MR * 2;
-    auto kern = paged_dec_kernel<Q8, NH, WR>;
+    p.part_ml = reinterpret_cast<float*>(ws + C::kParts * sizeof(int4));
+    p.part_o = p.part_ml + (size_t)2 * C::kParts * C::MR * 2;
+    auto kern = paged_dec_kernel<Q8, NH, NR, WR>;
     static SmemLimit limit;
     cudaError_t err = limit.raise(reinterpret_cast<const void*>(kern), C::kSmem);
     if (err != cudaSuccess) return err;
-    kern<<<kParts, kThreads, C::kSmem, s>>>(p);
+    kern<<<C::kParts, C::kThreads, C::kSmem, s>>>(p);
     err = cudaGetLastError();
     if (err != cudaSuccess || !p.split) return err;
     JoinParams j{p.c, p.out, p.lse, p.part_o, p.part_ml, p.desc, p.Hq, p.G};
-    return launch_paged_join<C::MR, C::D, kParts>(j, s);
+    return launch_paged_join<C::MR, C::D, C::kParts>(j, s);
 }
 
 template <bool Q8, int NH>
 cudaError_t by_rows(const PagedFwdArgs& a, cudaStream_t s) {
-    switch (rows_class(a.max_q, a.G)) {
-        case 1: return launch<Q8, NH, 1>(a, s);
-        case 2: return launch<Q8, NH, 2>(a, s);
-        default: return launch<Q8, NH, 4>(a, s);
+    switch (rows_of(a.max_q, a.G)) {
+        case 8: return launch<Q8, NH, 1, 1>(a, s);
+        case 16: return launch<Q8, NH, 2, 1>(a, s);
+        case 32: return launch<Q8, NH, 2, 2>(a, s);
+        default: return launch<Q8, NH, 2, 4>(a, s);
     }
 }
 
@@ -911,8 +989,9 @@ bool paged_dec_supported(const PagedFwdArgs& a) {
 }
 
 size_t paged_dec_workspace(int max_q, int G, int d) {
-    const size_t mr = 16 * rows_class(max_q, G), D = d <= 64 ? 64 : 128;
-    return kParts * sizeof(int4) + 2 * (size_t)kParts * mr * (D + 2) * sizeof(float);
+    const size_t mr = rows_of(max_q, G), D = d <= 64 ? 64 : 128;
+    const size_t parts = (mr == 8 ? 3 : 2) * 148;
+    return parts * sizeof(int4) + 2 * parts * mr * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_dec(const PagedFwdArgs& a, cudaStream_t s) {

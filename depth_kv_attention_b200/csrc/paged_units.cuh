@@ -2,7 +2,7 @@
 //
 // A unit is (sequence, kv-head, tile of MR rows); a row is a (token, head of
 // the group) pair of the sequence, flattened token-major, so every row of a
-// tile reads the same K and V. A unit's keys come in stages: 64 sequence keys
+// tile reads the same K and V. A unit's keys come in stages: KEYS sequence keys
 // each, then depth stages of DS slices of 16 slots of one token. All units'
 // stages form one list (sequence-major, then kv-head, then tile) that the
 // CTAs cut into equal parts, so a ragged batch loads every SM alike, whatever
@@ -51,7 +51,7 @@ struct UnitShape {
 // Tile rt of MR rows of a sequence with n tokens. DSL: 16-slot slices of one
 // token's depth rows; DS: slices per depth stage; max_keys: what the block
 // table can hold.
-template <int MR>
+template <int MR, int KEYS>
 __device__ __forceinline__ UnitShape unit_shape(const SeqInfo& s, int rt, int G, int DSL, int DS, long long max_keys) {
     UnitShape u;
     u.r0 = rt * MR;
@@ -60,16 +60,16 @@ __device__ __forceinline__ UnitShape unit_shape(const SeqInfo& s, int rt, int G,
     u.ntok = (u.r0 + u.rows - 1) / G - u.tok0 + 1;
     const long long last = (long long)s.pos0 + u.tok0 + u.ntok;  // position of the last token + 1
     u.nk = (int)max(0LL, min(last, max_keys));
-    u.st_seq = (u.nk + 63) / 64;
+    u.st_seq = (u.nk + KEYS - 1) / KEYS;
     u.st = max(u.st_seq + (u.ntok * DSL + DS - 1) / DS, 1);
     return u;
 }
 
-template <int MR>
+template <int MR, int KEYS>
 __device__ __forceinline__ long long seq_stages(const SeqInfo& s, int G, int DSL, int DS, long long max_keys) {
     long long t = 0;
     const int tiles = (s.n * G + MR - 1) / MR;
-    for (int rt = 0; rt < tiles; ++rt) t += unit_shape<MR>(s, rt, G, DSL, DS, max_keys).st;
+    for (int rt = 0; rt < tiles; ++rt) t += unit_shape<MR, KEYS>(s, rt, G, DSL, DS, max_keys).st;
     return t;
 }
 
