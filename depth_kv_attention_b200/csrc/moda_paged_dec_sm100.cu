@@ -63,7 +63,7 @@ struct DecParams {
     float* part_o;   // [2W][MR][D]
     float* part_ml;  // [2W][MR][2]
     int4* desc;      // [W]: {sequence, kv-head, tile, parts | rows << 16}, 0: no unit is cut there
-    int Hq, G, Ld, DSL, W, min_stages;
+    int Hq, G, Ld, DSL, W;
     int split;       // units may be cut (else each stays with one CTA)
     float sl2;
     unsigned int* status;
@@ -381,54 +381,95 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
             ptx::mbar_init(&bars->empty[s], C::kWarps);
         }
         bars->abort_flag = 0;
+        ptx::prefetch_tmap(&p.tm_k);
+        ptx::prefetch_tmap(&p.tm_v);
+        if (p.Ld > 0) {
+            ptx::prefetch_tmap(&p.tm_kd);
+            ptx::prefetch_tmap(&p.tm_vd);
+        }
         ptx::fence_barrier_init();
         ptx::fence_proxy_async_smem();
         p.desc[cta] = make_int4(0, 0, 0, 0);
     }
-    // ---- the list of stages: each thread sums a run of sequences, then a scan
-    const int per = (c.B + kThreads - 1) / kThreads;
-    const int b0 = min(threadIdx.x * per, c.B), b1 = min(b0 + per, c.B);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const SeqInfo s = seq_info(c, b);
-        if (b < kSeqs) bars->seqs[b] = s;
-        mine += seq_stages<C::MR, C::KEYS>(s, p.G, p.DSL, C::DS, max_keys);
-    }
+    // ---- the list of stages, and where this CTA's part of it begins
     auto seq_at = [&](int b) { return b < kSeqs ? bars->seqs[b] : seq_info(c, b); };
-    long long incl = mine * c.Hkv;
+    long long total, lo, hi, in_seq, seq_n;  // all stages; the part; its start and the stages per kv-head in its sequence
+    int b, W;
+    SeqInfo sq;
+    auto cut_list = [&]() {  // false: no part for this CTA
+        W = (int)max(1LL, min((long long)p.W, total));
+        if (cta >= W || total == 0) return false;
+        lo = part_begin(total, cta, W);
+        hi = part_begin(total, cta + 1, W);
+        return true;
+    };
+    if (c.B <= 32) {
+        // a sequence per lane, every warp for itself: one round of loads and no
+        // exchange through shared memory
+        SeqInfo mine = {0, 0, 0};
+        if (lane < c.B) mine = seq_info(c, lane);
+        const long long n = lane < c.B ? seq_stages<C::MR, C::KEYS>(mine, p.G, p.DSL, C::DS, max_keys) : 0;
+        if (warp == 0 && lane < c.B) bars->seqs[lane] = mine;
+        long long incl = n * c.Hkv;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) bars->scan[warp] = incl;
-    __syncthreads();
-    long long total = 0, pre = 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        total = __shfl_sync(0xffffffffu, incl, 31);
+        if (!cut_list()) return;
+        b = __ffs(__ballot_sync(0xffffffffu, lo < incl)) - 1;
+        in_seq = lo - __shfl_sync(0xffffffffu, incl - n * c.Hkv, b);
+        seq_n = __shfl_sync(0xffffffffu, n, b);
+        sq.q0 = __shfl_sync(0xffffffffu, mine.q0, b);
+        sq.n = __shfl_sync(0xffffffffu, mine.n, b);
+        sq.pos0 = __shfl_sync(0xffffffffu, mine.pos0, b);
+        __syncthreads();
+    } else {
+        // each thread sums a run of sequences, then a scan over the threads
+        const int per = (c.B + kThreads - 1) / kThreads;
+        const int b0 = min((int)threadIdx.x * per, c.B), b1 = min(b0 + per, c.B);
+        long long mine = 0;
+        for (int x = b0; x < b1; ++x) {
+            const SeqInfo s = seq_info(c, x);
+            if (x < kSeqs) bars->seqs[x] = s;
+            mine += seq_stages<C::MR, C::KEYS>(s, p.G, p.DSL, C::DS, max_keys);
+        }
+        long long incl = mine * c.Hkv;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) pre += bars->scan[w];
-        total += bars->scan[w];
-    }
-    incl += pre;
-    // parts: at least min_stages stages each
-    const int W = (int)max(1LL, min((long long)p.W, total / p.min_stages));
-    if (cta >= W || total == 0) return;
-    const long long lo = part_begin(total, cta, W), hi = part_begin(total, cta + 1, W);
-    {
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) bars->scan[warp] = incl;
+        __syncthreads();
+        total = 0;
+        long long pre = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) pre += bars->scan[w];
+            total += bars->scan[w];
+        }
+        incl += pre;
+        if (!cut_list()) return;
         long long at = incl - mine * c.Hkv;
-        if (lo >= at && lo < incl) {  // one thread: the CTA's part begins in its run
-            for (int b = b0; b < b1; ++b) {
-                const long long n = seq_stages<C::MR, C::KEYS>(seq_at(b), p.G, p.DSL, C::DS, max_keys) * c.Hkv;
+        if (lo >= at && lo < incl) {  // one thread: the part begins in its run
+            for (int x = b0; x < b1; ++x) {
+                const long long n = seq_stages<C::MR, C::KEYS>(seq_at(x), p.G, p.DSL, C::DS, max_keys) * c.Hkv;
                 if (lo < at + n) {
-                    bars->begin_seq = b;
+                    bars->begin_seq = x;
                     bars->begin_in_seq = lo - at;
                     break;
                 }
                 at += n;
             }
         }
+        __syncthreads();
+        b = bars->begin_seq;
+        in_seq = bars->begin_in_seq;
+        sq = seq_at(b);
+        seq_n = seq_stages<C::MR, C::KEYS>(sq, p.G, p.DSL, C::DS, max_keys);
     }
-    __syncthreads();
     volatile int* abort_flag = &bars->abort_flag;
     auto fail = [&]() {
         *abort_flag = 1;
@@ -436,21 +477,17 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
     };
 
     // ---- the units of this part, walked alike by every warp
-    int b = bars->begin_seq, kvh, rt = 0;
-    long long left = hi - lo;       // stages still to do
-    SeqInfo sq = seq_at(b);
-    int first;                      // first stage of the current unit's piece
-    {
-        long long in = bars->begin_in_seq;
-        const long long n = seq_stages<C::MR, C::KEYS>(sq, p.G, p.DSL, C::DS, max_keys);
-        kvh = (int)(in / n);
-        in -= (long long)kvh * n;
-        for (;; ++rt) {
-            const int st = unit_shape<C::MR, C::KEYS>(sq, rt, p.G, p.DSL, C::DS, max_keys).st;
-            if (in < st) break;
-            in -= st;
+    int kvh, rt = 0, first;     // first: first stage of the current unit's piece
+    long long left = hi - lo;   // stages still to do
+    if (in_seq < (1LL << 31) && seq_n < (1LL << 31)) kvh = (int)((uint32_t)in_seq / (uint32_t)seq_n);
+    else kvh = (int)(in_seq / seq_n);
+    for (long long in = in_seq - kvh * seq_n;; ++rt) {
+        const int st = unit_shape<C::MR, C::KEYS>(sq, rt, p.G, p.DSL, C::DS, max_keys).st;
+        if (in < st) {
+            first = (int)in;
+            break;
         }
-        first = (int)in;
+        in -= st;
     }
     auto next_unit = [&]() {
         first = 0;
@@ -896,7 +933,6 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
 }
 
 constexpr int kWholeKeys = 512;
-constexpr int kMinStages = 1;
 
 // Query rows of a unit by the rows a sequence has: 8, 16, 32 or 64.
 int rows_of(int max_q, int G) {
@@ -947,7 +983,6 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
     p.lse = a.lse;
     p.Hq = a.Hq; p.G = a.G; p.Ld = a.Ld; p.DSL = (a.Ld + kSliceRows - 1) / kSliceRows;
     p.W = C::kParts;
-    p.min_stages = kMinStages;
     // the longest unit the block table allows, in stages: short ones stay whole
     // and save the join
     p.split = (long long)c.max_blocks * c.page_size + (long long)a.Ld * ((C::MR + a.G - 2) / a.G + 1) > kWholeKeys;

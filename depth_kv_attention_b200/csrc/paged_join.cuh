@@ -36,7 +36,8 @@ __device__ __forceinline__ int join_passes(const int4& ds) {
 template <int MR, int D, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const JoinParams p) {
     constexpr int E = D / 32;
-    __shared__ int sums[kJoinWarps + 1], ends[W];
+    __shared__ int sums[kJoinWarps], ends[W];
+    __shared__ int4 descs[W];
     __shared__ float sml[kJoinWarps][2], so[kJoinWarps][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -45,7 +46,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const JoinP
     static_assert(kPer <= 64, "two loads a lane");
     const int at0 = warp * kPer + lane, at1 = at0 + 32;
     const bool in0 = lane < kPer && at0 < W, in1 = lane + 32 < kPer && at1 < W;
-    const int n0 = in0 ? join_passes(p.desc[at0]) : 0, n1 = in1 ? join_passes(p.desc[at1]) : 0;
+    int n0 = 0, n1 = 0;
+    if (in0) n0 = join_passes(descs[at0] = p.desc[at0]);
+    if (in1) n1 = join_passes(descs[at1] = p.desc[at1]);
     int i0 = n0, i1 = n1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -71,55 +74,87 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const JoinP
             if (ends[mid] <= item) lo = mid + 1; else hi = mid;
         }
         const int x = lo;
-        const int4 ds = p.desc[x];
+        const int4 ds = descs[x];
         const int parts = ds.w & 0xffff, rows = ds.w >> 16;
         const int pass = item - (x ? ends[x - 1] : 0);
         const bool shared = parts > kShareParts;
         const int r = shared ? pass : pass * kJoinWarps + warp;
         const int row = ds.z * MR + r;
         auto slot = [&](int i) { return (long long)(i == 0 ? 2 * x + 1 : 2 * (x + i)) * MR + r; };
+        const SeqInfo sq = seq_info(p.c, ds.x);
         float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
         if (r < rows) {
-            for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[slot(i) * 2]);
+            // eight parts at a time, all loads in flight together
+            constexpr int kBatch = 8;
+            const int step = shared ? kJoinWarps : 1;
+            for (int i0 = shared ? warp : 0; i0 < parts; i0 += kBatch * step) {
+                float2 ml[kBatch];
+                float v[kBatch][E];
+                float mn = m;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-            for (int i = shared ? warp : 0; i < parts; i += shared ? kJoinWarps : 1) {
-                const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(i) * 2);
-                const float w = ptx::ex2(ml.x - ref);
-                const float* po = p.part_o + slot(i) * D + lane * E;
-                l += ml.y * w;
-                if (E == 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(po);
-                    acc[0] += v.x * w; acc[1] += v.y * w; acc[E - 2] += v.z * w; acc[E - 1] += v.w * w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2*>(po);
-                    acc[0] += v.x * w; acc[1] += v.y * w;
+                for (int k = 0; k < kBatch; ++k) {
+                    const int i = i0 + k * step;
+                    ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[k][e] = 0.f;
+                    if (i < parts) {
+                        ml[k] = *reinterpret_cast<const float2*>(p.part_ml + slot(i) * 2);
+                        const float* po = p.part_o + slot(i) * D + lane * E;
+                        if (E == 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(po);
+                            v[k][0] = f.x; v[k][1] = f.y; v[k][E - 2] = f.z; v[k][E - 1] = f.w;
+                        } else {
+                            const float2 f = *reinterpret_cast<const float2*>(po);
+                            v[k][0] = f.x; v[k][1] = f.y;
+                        }
+                    }
                 }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
+                const float ref = mn == -INFINITY ? 0.f : mn, corr = ptx::ex2(m - ref);
+                l *= corr;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] *= corr;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float w = ptx::ex2(ml[k].x - ref);
+                    l += ml[k].y * w;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] += v[k][e] * w;
+                }
+                m = mn;
             }
         }
         if (shared) {  // the eight warps' sums, in their order
 #pragma unroll
             for (int e = 0; e < E; ++e) so[warp][lane * E + e] = acc[e];
-            if (lane == 0) sml[warp][1] = l;
+            if (lane == 0) {
+                sml[warp][0] = m;
+                sml[warp][1] = l;
+            }
             __syncthreads();
-            l = 0.f;
+            if (warp == 0) {
+                m = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = 0.f;
-            if (warp == 0)
+                for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, sml[w][0]);
+                const float ref = m == -INFINITY ? 0.f : m;
+                l = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
                 for (int w = 0; w < kJoinWarps; ++w) {
-                    l += sml[w][1];
+                    const float c = ptx::ex2(sml[w][0] - ref);
+                    l += sml[w][1] * c;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += so[w][lane * E + e];
+                    for (int e = 0; e < E; ++e) acc[e] += so[w][lane * E + e] * c;
                 }
+            }
             __syncthreads();
         }
         if (r < rows && (!shared || warp == 0)) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const SeqInfo sq = seq_info(p.c, ds.x);
             const long long orow = (long long)(sq.q0 + row / p.G) * p.Hq + ds.y * p.G + row % p.G;
 #pragma unroll
             for (int e = 0; e < E; e += 2)
