@@ -644,8 +644,8 @@ size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, 
         return 0;
     if (dtype != MODA_BF16 || page_size % 16) return 0;
     const size_t dec = paged_dec_workspace(max_q, Hq / Hkv, d);
-    if ((long long)max_q * (Hq / Hkv) < kPagedPreRows || d != 128) return dec;
-    const size_t pre = paged_pre_workspace(Hkv, num_pages, page_size, q8 != 0);
+    if ((long long)max_q * (Hq / Hkv) < kPagedPreRows || Hq / Hkv > 128) return dec;
+    const size_t pre = paged_pre_workspace(Hkv, d, num_pages, page_size, q8 != 0);
     return pre > dec ? pre : dec;
 }
 

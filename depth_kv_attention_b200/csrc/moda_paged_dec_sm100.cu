@@ -1000,7 +1000,7 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
     kern<<<C::kParts, C::kThreads, C::kSmem, s>>>(p);
     err = cudaGetLastError();
     if (err != cudaSuccess || !p.split) return err;
-    JoinParams j{p.c, p.out, p.lse, p.part_o, p.part_ml, p.desc, p.Hq, p.G};
+    JoinParams j{p.c, p.out, p.lse, p.part_o, p.part_ml, p.desc, p.Hq, p.G, 0};
     return launch_paged_join<C::MR, C::D, C::kParts>(j, s);
 }
 

@@ -1,5 +1,5 @@
 // Attention over the paged sequence cache for many query rows per sequence
-// (chunks of prompts, wide drafts): d = 128, on tcgen05. bf16 pages; 8-bit ones
+// (chunks of prompts, wide drafts), on tcgen05. bf16 pages; 8-bit ones
 // are turned into bf16 once, ahead of it (see the end of the file).
 //
 // What it computes: as moda_paged_dec_sm100.cu, one softmax over the sequence
@@ -38,7 +38,7 @@
 namespace moda {
 namespace {
 
-constexpr int kD = 128;
+constexpr int kD = 128;         // features of a tile; rows of fewer are padded with zeros by TMA
 constexpr int kTileBytes = 128 * kD * 2;
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kRows = 256;      // rows of a unit: two tiles
@@ -60,7 +60,9 @@ struct PreParams {
     float* part_o;
     float* part_ml;
     int4* desc;
-    int Hq, G, n, lg_step, Ld, Ld_cap, DSL;  // a unit has 2n = 1 << lg_step tokens
+    int Hq, G, n, Ld, Ld_cap, DSL;  // a tile has n tokens, n * G of its 128 rows
+    int lg_step;                    // 2n = 1 << lg_step <= 128, or -1
+    int halves;                     // 64-feature halves of a row in use
     int box_rows;  // rows of a page box: the largest power of two that divides the page size, at most 128
     float sl2;
     unsigned int* status;
@@ -135,32 +137,54 @@ __device__ __forceinline__ Unit make_unit(const PreParams& p, const SeqInfo& s, 
     return u;
 }
 
+// Sum of floor((a i + b) / m) over i < n, by Euclid's algorithm on (a, m).
+__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+    long long t = 0;
+    for (;;) {
+        t += (n - 1) * n / 2 * (a / m) + n * (b / m);
+        a %= m;
+        b %= m;
+        const long long y = a * n + b;
+        if (y < m) return t;
+        n = y / m;
+        b = y % m;
+        const long long x = m;
+        m = a;
+        a = x;
+    }
+}
 // Items of the sequence's first `tiles` units. Unit rt sees
 // min(pos0 + 2n (rt + 1), pos0 + n_tokens) keys; where no unit is clipped by
-// position 0 or by the table, ceil(keys / 128) over the whole units is a sum
-// of floor(t / m) over consecutive t (2n is a power of two that divides 128 m
-// or is 256), so it needs no loop.
+// position 0 or by the table, ceil(keys / 128) over the whole units is a sum of
+// floors, so it needs no loop over them. With 2n a power of two that divides
+// 128 the floors are those of t / m, m = 128 / 2n, over consecutive t.
 __device__ __forceinline__ long long items_before(const PreParams& p, const SeqInfo& s, int tiles, long long max_keys) {
-    const int step = 1 << p.lg_step;  // 2n
+    const int step = 2 * p.n;
     const long long last = (long long)s.pos0 + s.n;
-    if (s.pos0 < 0 || last > max_keys || step > kItemKeys) {
+    if (s.pos0 < 0 || last > max_keys) {
         long long t = 0;
         for (int rt = 0; rt < tiles; ++rt) t += make_unit(p, s, rt, max_keys).n_items;
         return t;
     }
-    const int whole = min(tiles, s.n >> p.lg_step);
-    const int lg_m = 7 - p.lg_step, m = 1 << lg_m;
-    const int q = (int)(((long long)s.pos0 + step + kItemKeys - 1) >> p.lg_step);  // ceil(K / 128) = floor((q + rt) / m)
-    auto f = [&](int x) {                                        // sum of floor(t / m), t < x
-        const long long k = x >> lg_m;
-        return ((k * (k - 1) / 2) << lg_m) + k * (x & (m - 1));
-    };
-    long long t = f(q + whole) - f(q) + (long long)whole * ((step * p.DSL + kSlices - 1) / kSlices);
+    const int whole = min(tiles, p.lg_step >= 0 ? s.n >> p.lg_step : s.n / step);
+    long long t;
+    if (p.lg_step >= 0) {
+        const int lg_m = 7 - p.lg_step, m = 1 << lg_m;
+        const int q = (int)(((long long)s.pos0 + step + kItemKeys - 1) >> p.lg_step);  // ceil(K / 128) = floor((q + rt) / m)
+        auto f = [&](int x) {                                                          // sum of floor(t / m), t < x
+            const long long k = x >> lg_m;
+            return ((k * (k - 1) / 2) << lg_m) + k * (x & (m - 1));
+        };
+        t = f(q + whole) - f(q);
+    } else {
+        t = whole ? floor_sum(whole, kItemKeys, step, (long long)s.pos0 + step + kItemKeys - 1) : 0;
+    }
+    t += (long long)whole * ((step * p.DSL + kSlices - 1) / kSlices);
     if (tiles > whole) t += make_unit(p, s, whole, max_keys).n_items;
     return t;
 }
 __device__ __forceinline__ long long seq_items(const PreParams& p, const SeqInfo& s, long long max_keys) {
-    return items_before(p, s, (s.n + 2 * p.n - 1) >> p.lg_step, max_keys);
+    return items_before(p, s, (s.n + 2 * p.n - 1) / (2 * p.n), max_keys);
 }
 __device__ __forceinline__ long long table_keys(const PagedCache& c) {
     return min((long long)c.max_blocks * c.page_size, 0x7fffff00LL);
@@ -214,11 +238,11 @@ __device__ __forceinline__ bool next_piece(Walk* w, const PreParams& p, int lane
 // Sets the non-finite elements of a bf16 value tile to 0. Returns whether this
 // thread met one in a row below `rows` (rows past it nobody sees). The usual
 // tile has none: 0 * x summed over everything is NaN exactly when one is there.
-__device__ __forceinline__ bool clear_nonfinite(uint8_t* slot, int ct, int rows) {
+__device__ __forceinline__ bool clear_nonfinite(uint8_t* slot, int ct, int rows, int halves) {
     const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
     __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
 #pragma unroll 8
-    for (int ch = ct; ch < kTileBytes / 16; ch += kCond) {
+    for (int ch = ct; ch < halves * (kHalfBytes / 16); ch += kCond) {
         const uint4 v = *reinterpret_cast<const uint4*>(slot + ch * 16);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -232,7 +256,7 @@ __device__ __forceinline__ bool clear_nonfinite(uint8_t* slot, int ct, int rows)
     const float2 f = __bfloat1622float2(sum);
     if (f.x == 0.f && f.y == 0.f) return false;
     bool met = false;
-    for (int ch = ct; ch < kTileBytes / 16; ch += kCond) {
+    for (int ch = ct; ch < halves * (kHalfBytes / 16); ch += kCond) {
         uint4* at = reinterpret_cast<uint4*>(slot + ch * 16);
         const uint4 v = *at;
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -328,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                     long long in = lo - at;
                     w.kvh = (int)(in / k);
                     in -= w.kvh * k;
-                    int x = 0, y = ((w.sq.n + 2 * p.n - 1) >> p.lg_step) - 1;  // last unit that starts at or before `in`
+                    int x = 0, y = (w.sq.n + 2 * p.n - 1) / (2 * p.n) - 1;  // last unit that starts at or before `in`
                     while (x < y) {
                         const int mid = (x + y + 1) / 2;
                         if (items_before(p, w.sq, mid, max_keys) <= in) x = mid; else y = mid - 1;
@@ -406,13 +430,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                     used |= bit;
                     if (kv == 0 && lane == 0) bars->holes[item % kMeta] = seq ? none : 0;
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, kTileBytes);
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, p.halves * kHalfBytes);
                     __syncwarp();
                     if (seq) {
                         // boxes of box_rows rows and half of the features
                         const int half = lane & 1, r0 = (lane >> 1) * p.box_rows;
                         const int pg = __shfl_sync(0xffffffffu, page, ((rel & 31) + (r0 >> 4)) & 31);
-                        if (r0 < kItemKeys)
+                        if (r0 < kItemKeys && half < p.halves)
                             // a page that is not there lies outside the map: zeros
                             ptx::tma_load_4d(dst + half * kHalfBytes + r0 * 128, kv ? &p.tm_v : &p.tm_k, bar, half * 64,
                                              pg < 0 ? 0 : (x * kItemKeys + r0) % c.page_size, kvh,
@@ -421,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                         const int sl = lane & 7, half = (lane >> 3) & 1;
                         const int y = (x - n_seq) * kSlices + sl;
                         const int tok = p.DSL ? y / p.DSL : 0, s16 = p.DSL ? y % p.DSL : 0;
-                        if (lane < 16)
+                        if (lane < 16 && half < p.halves)
                             ptx::tma_load_4d(dst + half * kHalfBytes + sl * 2048, kv ? &p.tm_vd : &p.tm_kd, bar,
                                              half * 64, kvh, s16 * 16, p.DSL && tok < ntok ? row0 + tok : c.N);
                     }
@@ -439,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                             break;
                         }
                     }
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->q_full, 2 * kTileBytes);
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->q_full, 2 * p.halves * n * p.G * 128);
                     __syncwarp();
-                    if (lane < 4)
+                    if (lane < 4 && (lane & 1) < p.halves)
                         ptx::tma_load_4d(sQ + (lane >> 1) * kTileBytes + (lane & 1) * kHalfBytes, &p.tm_q, &bars->q_full,
                                  (lane & 1) * 64, kvh * p.G, row0 + (lane >> 1) * n, 0);
                     q_par = piece + 1;  // query loads issued
@@ -460,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
         // ------------------------------------------------------ MMA thread
         if (lane == 0) {
             constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, kItemKeys, 0, 0);
-            constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, kD, 0, 1);
+            const uint32_t idesc_pv = ptx::idesc_bf16_f32(128, p.halves * 64, 0, 1);
+            const bool two_halves = p.halves == 2;
             const uint32_t sQa = ptx::smem_u32(sQ), sRa = ptx::smem_u32(sRing);
             const uint64_t q0 = ptx::umma_desc_sw128(sQa, 16, 1024);
             const uint64_t k0 = ptx::umma_desc_sw128(sRa, 16, 1024);
@@ -474,10 +499,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
             };
             auto issue_s = [&](int i, int st) {
                 const uint64_t kd_ = k0 + (uint64_t)st * kSlotUnits, qd_ = q0 + (uint64_t)i * kSlotUnits;
+                // both halves of the features, or the first alone
+                if (two_halves) {
 #pragma unroll
-                for (int k = 0; k < kD / 16; ++k) {
-                    const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
-                    ptx::mma_ss(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0);
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
+                        ptx::mma_ss(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) ptx::mma_ss(tmem + i * 128, qd_ + k * 2, kd_ + k * 2, idesc_qk, k > 0);
                 }
                 ptx::mma_commit(&bars->s_full[i]);
             };
@@ -596,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                             break;
                         }
                         const int rows = seq ? min(nk - x * kItemKeys, kItemKeys) : kItemKeys;
-                        if (clear_nonfinite(slot, ct, rows)) bars->bad_piece[piece % kMeta] = piece;
+                        if (clear_nonfinite(slot, ct, rows, p.halves)) bars->bad_piece[piece % kMeta] = piece;
                         ptx::fence_proxy_async_smem();
                         ptx::bar_sync(1, kCond);
                         if (ct == 0) ptx::mbar_arrive(full);
@@ -612,7 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
         const int r = (warp % 4) * 32 + lane;
         const uint32_t lane_off = (uint32_t)((warp % 4) * 32) << 16;
         const uint32_t tS = tmem + lane_off + i * 128, tO = tmem + lane_off + 256 + i * 128;
-        const int tl = i * n + r / p.G;       // token of the unit
+        const bool used = r < n * p.G;        // (n G may be less than 128)
+        const int tl = used ? i * n + r / p.G : 2 * n;  // token of the unit
         const int hh = r % p.G;
         bool ok = true;
         uint32_t sp = 0;                      // s_full phase
@@ -620,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
         Walk* w = walks + warp;
         for (bool more = true; more && ok; more = next_piece(w, p, lane)) {
             const int first = w->first, end = w->end, piece = w->piece, n_seq = w->u.n_seq;
-            const int pos = w->sq.pos0 + w->u.tok0 + tl;
+            const int pos = used ? w->sq.pos0 + w->u.tok0 + tl : -1;
             float m = -INFINITY, l = 0.f;
             int it = 0;
             // this tile's items: sequence items below nkv, depth items [dlo, dhi)
@@ -681,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
             const long long row = (long long)(w->sq.q0 + w->u.tok0 + tl) * p.Hq + kvh * p.G + hh;
             const bool bad = *reinterpret_cast<volatile int*>(&bars->bad_piece[piece % kMeta]) == piece;
 #pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
+            for (int cc = 0; cc < 4 && cc * 32 < c.d; ++cc) {
                 uint32_t o[32];
                 if (it > 0) {
                     ptx::tmem_ld32(tO + cc * 32, o);
@@ -695,6 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                     auto add = [&](const __nv_bfloat16* v) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
+                            if (cc * 32 + e >= c.d) break;
                             const float f = __bfloat162float(v[cc * 32 + e]);
                             if (!(fabsf(f) <= 3.4e38f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
                         }
@@ -705,13 +738,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                         for (int j = x0 * kItemKeys; j < min(x1 * kItemKeys, min(pos + 1, w->u.nk)); ++j) {
                             const int pg = page_of(c, w->b, j / c.page_size);
                             if (pg >= 0)
-                                add(p.v_pages + (((long long)pg * c.Hkv + kvh) * c.page_size + j % c.page_size) * kD);
+                                add(p.v_pages + (((long long)pg * c.Hkv + kvh) * c.page_size + j % c.page_size) * c.d);
                         }
                     }
                     for (int s = 0; s < p.Ld; ++s) {
                         const int xi = n_seq + (tl * p.DSL + s / 16) / kSlices;
                         if (xi >= first && xi < end)
-                            add(p.vd + (((long long)(w->sq.q0 + w->u.tok0 + tl) * p.Ld_cap + s) * c.Hkv + kvh) * kD);
+                            add(p.vd + (((long long)(w->sq.q0 + w->u.tok0 + tl) * p.Ld_cap + s) * c.Hkv + kvh) * c.d);
                     }
                 }
                 if (!valid) continue;
@@ -720,9 +753,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         q[e] = ptx::pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + row * kD + cc * 32);
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + row * c.d + cc * 32);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) dst[v] = make_uint4(q[4 * v], q[4 * v + 1], q[4 * v + 2], q[4 * v + 3]);
+                    for (int v = 0; v < 4; ++v)
+                        if (cc * 32 + 8 * v < c.d) dst[v] = make_uint4(q[4 * v], q[4 * v + 1], q[4 * v + 2], q[4 * v + 3]);
                 } else {
                     float* dst = p.part_o + ((long long)ps * kRows + i * 128 + r) * kD + cc * 32;
 #pragma unroll
@@ -734,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                     // parts of the unit, up to the one that holds its last item
                     const long long last = bars->hi - w->left + w->u.n_items;
                     const int c_last = (int)((last * bars->W + bars->total - 1) / bars->total) - 1;
-                    p.desc[cta] = make_int4(w->b, kvh, w->rt, (c_last - cta + 1) | min(w->u.ntok * p.G, kRows) << 16);
+                    p.desc[cta] = make_int4(w->b, kvh, w->rt, (c_last - cta + 1) | (w->u.ntok <= n ? w->u.ntok * p.G : 128 + (w->u.ntok - n) * p.G) << 16);
                 }
                 if (!whole)
                     *reinterpret_cast<float2*>(p.part_ml + ((long long)ps * kRows + i * 128 + r) * 2) = make_float2(m, l);
@@ -762,24 +796,28 @@ cudaError_t launch(const PagedFwdArgs& a, char* ws, cudaStream_t s) {
     const PagedCache& c = a.c;
     const cuuint64_t P = c.page_size, Hkv = c.Hkv;
     p.n = 128 / a.G;
-    for (p.lg_step = 0; (1 << p.lg_step) < 2 * p.n;) ++p.lg_step;
+    p.lg_step = -1;
+    for (int lg = 1; lg <= 7; ++lg)
+        if (2 * p.n == 1 << lg) p.lg_step = lg;
+    p.halves = c.d <= 64 ? 1 : 2;
+    const cuuint64_t d = c.d;
     {
-        const cuuint64_t dims[4] = {kD, (cuuint64_t)a.Hq, (cuuint64_t)c.N, 1};
-        const cuuint64_t st[3] = {kD * 2, (cuuint64_t)a.Hq * kD * 2, (cuuint64_t)c.N * a.Hq * kD * 2};
+        const cuuint64_t dims[4] = {d, (cuuint64_t)a.Hq, (cuuint64_t)c.N, 1};
+        const cuuint64_t st[3] = {d * 2, (cuuint64_t)a.Hq * d * 2, (cuuint64_t)c.N * a.Hq * d * 2};
         const cuuint32_t box[4] = {64, (cuuint32_t)a.G, (cuuint32_t)p.n, 1};
         if (!make_tmap_bf16_4d(&p.tm_q, a.q, dims, st, box)) return cudaErrorInvalidValue;
     }
     {
-        const cuuint64_t dims[4] = {kD, P, Hkv, (cuuint64_t)c.num_pages};
-        const cuuint64_t st[3] = {kD * 2, P * kD * 2, Hkv * P * kD * 2};
+        const cuuint64_t dims[4] = {d, P, Hkv, (cuuint64_t)c.num_pages};
+        const cuuint64_t st[3] = {d * 2, P * d * 2, Hkv * P * d * 2};
         p.box_rows = std::min(c.page_size & -c.page_size, kItemKeys);
         const cuuint32_t box[4] = {64, (cuuint32_t)p.box_rows, 1, 1};
         if (!make_tmap_bf16_4d(&p.tm_k, a.k_pages, dims, st, box) || !make_tmap_bf16_4d(&p.tm_v, a.v_pages, dims, st, box))
             return cudaErrorInvalidValue;
     }
     if (a.Ld > 0) {
-        const cuuint64_t dims[4] = {kD, Hkv, (cuuint64_t)a.Ld, (cuuint64_t)c.N};
-        const cuuint64_t st[3] = {kD * 2, Hkv * kD * 2, (cuuint64_t)a.Ld_cap * Hkv * kD * 2};
+        const cuuint64_t dims[4] = {d, Hkv, (cuuint64_t)a.Ld, (cuuint64_t)c.N};
+        const cuuint64_t st[3] = {d * 2, Hkv * d * 2, (cuuint64_t)a.Ld_cap * Hkv * d * 2};
         const cuuint32_t box[4] = {64, 1, 16, 1};
         if (!make_tmap_bf16_4d(&p.tm_kd, a.kd, dims, st, box) || !make_tmap_bf16_4d(&p.tm_vd, a.vd, dims, st, box))
             return cudaErrorInvalidValue;
@@ -806,7 +844,7 @@ cudaError_t launch(const PagedFwdArgs& a, char* ws, cudaStream_t s) {
     paged_pre_kernel<<<kParts, kThreads, kSmemBytes, s>>>(p);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    JoinParams j{p.c, p.out, p.lse, p.part_o, p.part_ml, p.desc, p.Hq, p.G};
+    JoinParams j{p.c, p.out, p.lse, p.part_o, p.part_ml, p.desc, p.Hq, p.G, p.n};
     return launch_paged_join<kRows, kD, kParts>(j, s);
 }
 
@@ -832,8 +870,8 @@ __global__ void __launch_bounds__(256) paged_dequant_kernel(const PagedCache c, 
         if (page < 0) continue;
         const long long row = (long long)page * c.Hkv + h;
         const float k1 = __ldg(ks + row), v1 = __ldg(vs + row);
-        const long long at = row * c.page_size * kD;
-        const int n16 = (int)min((long long)c.page_size, keys - (long long)blk * c.page_size) * (kD / 16);
+        const long long at = row * c.page_size * c.d;
+        const int n16 = (int)min((long long)c.page_size, keys - (long long)blk * c.page_size) * (c.d / 16);
         for (int e = threadIdx.x; e < n16; e += blockDim.x) {
             const uint4 a = *reinterpret_cast<const uint4*>(kc + at + e * 16), d = *reinterpret_cast<const uint4*>(vc + at + e * 16);
             auto put = [&](const uint4& w, float sc, __nv_bfloat16* dst) {
@@ -856,8 +894,8 @@ __global__ void __launch_bounds__(256) paged_dequant_kernel(const PagedCache c, 
 size_t join_bytes() {
     return kParts * sizeof(int4) + 2 * (size_t)kParts * kRows * (kD + 2) * sizeof(float) + 32;
 }
-size_t pool_bytes(int Hkv, long long num_pages, int page_size) {
-    return ((size_t)num_pages * Hkv * page_size * kD * 2 + 255) & ~size_t(255);
+size_t pool_bytes(int Hkv, long long num_pages, int page_size, int d) {
+    return ((size_t)num_pages * Hkv * page_size * d * 2 + 255) & ~size_t(255);
 }
 
 }  // namespace
@@ -865,13 +903,13 @@ size_t pool_bytes(int Hkv, long long num_pages, int page_size) {
 bool paged_pre_supported(const PagedFwdArgs& a) {
     // (a scale <= 0 goes to the other kernels: the dense softmax step takes a
     // row's maximum before it scales)
-    return a.dtype == MODA_BF16 && a.c.d == kD && a.G <= 128 && 128 % a.G == 0 && a.c.page_size % 16 == 0 && a.scale > 0.f &&
+    return a.dtype == MODA_BF16 && a.c.d % 8 == 0 && a.G <= 128 && a.c.page_size % 16 == 0 && a.scale > 0.f &&
            (long long)a.c.N * a.Hq < (1LL << 31);
 }
 
-size_t paged_pre_workspace(int Hkv, long long num_pages, int page_size, bool q8) {
+size_t paged_pre_workspace(int Hkv, int d, long long num_pages, int page_size, bool q8) {
     const size_t parts = (join_bytes() + 255) & ~size_t(255);
-    return q8 ? parts + 2 * pool_bytes(Hkv, num_pages, page_size) + 32 : parts;
+    return q8 ? parts + 2 * pool_bytes(Hkv, num_pages, page_size, d) + 32 : parts;
 }
 
 cudaError_t launch_paged_pre(const PagedFwdArgs& a, cudaStream_t s) {
@@ -880,7 +918,7 @@ cudaError_t launch_paged_pre(const PagedFwdArgs& a, cudaStream_t s) {
     // [parts | bf16 K pages | bf16 V pages], the pages at 32-byte boundaries
     const PagedCache& c = a.c;
     char* pages = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws + ((join_bytes() + 255) & ~size_t(255))) + 31) & ~uintptr_t(31));
-    const size_t pool = pool_bytes(c.Hkv, c.num_pages, c.page_size);
+    const size_t pool = pool_bytes(c.Hkv, c.num_pages, c.page_size, c.d);
     PagedFwdArgs f = a;
     f.k_pages = pages;
     f.v_pages = pages + pool;

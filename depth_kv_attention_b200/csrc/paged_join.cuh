@@ -19,6 +19,7 @@ struct JoinParams {
     const float* part_ml;  // [2W][MR][2]
     const int4* desc;      // [W]: {sequence, kv-head, tile, parts | rows << 16}, 0: no unit is cut there
     int Hq, G;
+    int n;  // tokens of a 128-row tile (rows past n G unused), or 0: rows are (token, head) without gaps
 };
 
 // Joins the parts of cut units, always in their order. Every block lists the
@@ -79,13 +80,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const JoinP
         const int pass = item - (x ? ends[x - 1] : 0);
         const bool shared = parts > kShareParts;
         const int r = shared ? pass : pass * kJoinWarps + warp;
-        const int row = ds.z * MR + r;
+        // row r of the tile: token and head
+        const int rr = p.n ? r & 127 : ds.z * MR + r;
+        const int tok = p.n ? (2 * ds.z + (r >> 7)) * p.n + rr / p.G : rr / p.G;
+        const bool there = r < rows && (!p.n || rr < p.n * p.G);
         auto slot = [&](int i) { return (long long)(i == 0 ? 2 * x + 1 : 2 * (x + i)) * MR + r; };
         const SeqInfo sq = seq_info(p.c, ds.x);
         float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        if (r < rows) {
+        if (there) {
             // eight parts at a time, all loads in flight together
             constexpr int kBatch = 8;
             const int step = shared ? kJoinWarps : 1;
@@ -153,9 +157,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const JoinP
             }
             __syncthreads();
         }
-        if (r < rows && (!shared || warp == 0)) {
+        if (there && (!shared || warp == 0)) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const long long orow = (long long)(sq.q0 + row / p.G) * p.Hq + ds.y * p.G + row % p.G;
+            const long long orow = (long long)(sq.q0 + tok) * p.Hq + ds.y * p.G + rr % p.G;
 #pragma unroll
             for (int e = 0; e < E; e += 2)
                 if (lane * E + e < p.c.d)

@@ -441,8 +441,8 @@ moda_status moda_paged_append_q8(const void* q, const void* k, const void* v,
  *   workspace  in  device scratch of >= moda_fwd_paged_workspace_bytes(...),
  *                  16-byte aligned, contents on entry ignored (may be NULL
  *                  when that is 0). Calls that share it must not overlap. For
- *                  chunks over 8-bit pages (max_q * G of 65 and more, d = 128;
- *                  q8 != 0 in the size's call) it also holds the pages in use
+ *                  chunks over 8-bit pages (max_q * G of 65 and more; q8 != 0 in
+ *                  the size's call) it also holds the pages in use
  *                  as bf16, in two pools of num_pages pages; one workspace
  *                  serves all layers.
  * The attention does not append: call moda_paged_append first, with the same

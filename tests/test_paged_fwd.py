@@ -38,6 +38,14 @@ CASES = [
     Paged("chunk_g8", ((700, 300), (90, 33)), Hq=8, Hkv=1, Ld=16, cap=16, P=64),
     Paged("chunk_g1", ((300, 150),), Hq=2, Hkv=2, Ld=7, cap=7, d=128),
     Paged("chunk_g7", ((300, 90),), Hq=7, Hkv=1, Ld=2, cap=2, d=96),
+    Paged("chunk_g5_d64", ((330, 70), (20, 20), (9, 0)), Hq=10, Hkv=2, Ld=5, cap=6, d=64, P=32),
+    Paged("chunk_g3_d72", ((150, 150), (33, 32)), Hq=3, Hkv=1, Ld=17, cap=17, d=72, spare_rows=1),
+    Paged("chunk_g71", ((60, 9), (130, 2)), Hq=71, Hkv=1, Ld=2, cap=2, P=128),
+    Paged("chunk_g100_d8", ((40, 5),), Hq=100, Hkv=1, Ld=1, cap=1, d=8),
+    Paged("chunk_g130", ((40, 3),), Hq=130, Hkv=1, d=64),
+    Paged("chunk_many", tuple((20 + 7 * b, (5 * b) % 17) for b in range(40)), Hq=12, Hkv=2, Ld=3, cap=3),
+    Paged("chunk_short_ctx", ((5, 70), (3, 40), (0, 30)), Hq=4, Hkv=1),
+    Paged("chunk_short_depth", ((5, 70), (3, 40), (0, 30)), Hq=4, Hkv=1, Ld=4, cap=4),
     Paged("deep", steps(40), Hq=4, Hkv=1, Ld=130, cap=140),
     Paged("short_ctx", ((2, 5), (0, 1), (3, 3)), Hq=8, Hkv=2),
     Paged("short_ctx_depth", ((2, 5), (0, 1), (3, 3)), Hq=8, Hkv=2, Ld=3, cap=3),
@@ -128,6 +136,65 @@ def test_nan_where_a_row_does_not_look():
     ok = [0, 1]
     check_rows(out[ok], lse[ok], tuple(w[ok] for w in clean), c.dtype, keys_of(c), c.d)
     assert torch.isnan(out[2:]).all() and torch.isnan(lse[3]).all()
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
+@pytest.mark.parametrize("G", [8, 7])
+def test_nan_in_a_chunk(G, q8):
+    """The same in a chunk of many rows, whose tiles of 128 keys are masked row
+    by row: a non-finite value of a late token and of one token's depth rows
+    reaches exactly the rows and features that see it."""
+    c = Paged("nanchunk", ((300, 120), (90, 40)), Hq=G, Hkv=1, Ld=3, cap=3, d=96)
+    x = make(c, q8=q8)
+    clean = want(x, c)
+    at = 250                                             # position of new token 70 of sequence 0
+    if not q8:
+        x["v_pages"][int(x["table"][0, at // 16]), :, at % 16, 5] = float("inf")
+    x["vd"][33, 1, 0, 7] = float("nan")
+    out, lse = run(cuda(x), c, q8)
+    torch.cuda.synchronize()
+    assert moda.moda_device_status() == 0
+    hit = torch.zeros(c.N, G, c.d, dtype=torch.bool)
+    if not q8:
+        hit[70:120, :, 5] = True
+        assert torch.isinf(out[70:120, :, 5]).all()
+    hit[33, :, 7] = True
+    assert torch.isnan(out[33, :, 7]).all()
+    got = torch.where(hit.cuda(), torch.tensor(0.0, dtype=out.dtype, device="cuda"), out)
+    o, l, a, z = clean
+    o, a = o.copy(), a.copy()
+    o[hit.numpy()], a[hit.numpy()] = 0.0, 1.0
+    check_rows(got, lse, (o, l, a, z), c.dtype, keys_of(c), c.d)
+
+
+@pytest.mark.parametrize("seqs", [((900, 1), (400, 1)), ((300, 90),)], ids=["steps", "chunk"])
+def test_expired_waits_are_reported(seqs):
+    """Every wait in the kernels is bounded: with a cap of one poll they give
+    up, the call ends and the status word says so; the next call is sound."""
+    c = Paged("limit", seqs, Hq=8, Hkv=1, Ld=2, cap=2)
+    x = make(c)
+    g = cuda(x)
+    torch.cuda.synchronize()
+    moda.moda_debug_set_wait_limit(1)
+    try:
+        run(g, c, False)
+        assert moda.moda_device_status() == 6
+    finally:
+        moda.moda_debug_set_wait_limit(0)
+    got = run(g, c, False)
+    assert moda.moda_device_status() == 0
+    check_rows(*got, want(x, c), c.dtype, keys_of(c), c.d)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_scale_of_zero_and_below(scale):
+    c = Paged("scale", ((60, 30), (33, 1)), Hq=8, Hkv=1, d=64)
+    x = make(c)
+    out, lse = moda.moda_fwd_paged(*(x[n].cuda() for n in ("q", "k_pages", "v_pages", "table", "cu_q", "ctx")), 30,
+                                   scale=scale)
+    torch.cuda.synchronize()
+    w = oracle.paged_forward(x["q"], x["k_pages"], x["v_pages"], x["table"], x["cu_q"], x["ctx"], None, None, 0, scale)
+    check_rows(out, lse, w, c.dtype, keys_of(c), c.d)
 
 
 @pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
