@@ -374,7 +374,6 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
     const long long max_keys = min((long long)c.max_blocks * c.page_size, 0x7fffff00LL);
     const int cta = blockIdx.x;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NS; ++s) {
             ptx::mbar_init(&bars->full[s], 1);
@@ -930,6 +929,9 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
         left -= end - first;
         if (left > 0) next_unit();
     }
+    // the join may be scheduled once every CTA is about here; earlier its
+    // waiting blocks would take issue slots from this kernel
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 constexpr int kWholeKeys = 512;

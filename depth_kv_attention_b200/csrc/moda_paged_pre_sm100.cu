@@ -48,6 +48,8 @@ constexpr int kParts = 148;     // one CTA per SM
 constexpr int kMeta = 8;        // items whose slice notes are kept (the rings hold fewer than 5)
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kPieces = 8;      // pieces described at a time
+constexpr int kPieceUsers = 11; // warps that read a piece: softmax 8, MMA, conditioning 2
 constexpr uint32_t kNoPollLimit = 0;
 
 struct PreParams {
@@ -80,10 +82,11 @@ constexpr int kControlRegs = 72;
 constexpr int kStages = 5;
 
 struct __align__(8) PreBars {
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];
     uint64_t full[kStages], empty[kStages];
     uint64_t raw_full[kStages];      // a value tile that is to be conditioned has landed
     uint64_t s_full[2], p_full[2], o_final[2], o_empty[2];
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
     uint64_t drain;
     uint32_t holes[kMeta];           // per item: slices without a page
     int bad_piece[kMeta];            // last piece that met a non-finite value a row may see
@@ -94,7 +97,6 @@ struct __align__(8) PreBars {
     int abort_flag;
 };
 constexpr int kCtl = 2048;
-constexpr int kWalks = 12;  // one per warp
 constexpr int kSmemBytes = (2 + kStages) * kTileBytes + kCtl + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 
@@ -103,15 +105,29 @@ __device__ __forceinline__ void flag_timeout(PreParams const& p, PreBars* bars) 
     atomicOr(p.status, 1u);
 }
 
-// A unit: tokens tok0 .. tok0 + ntok - 1 of a sequence (tile i: n of them).
+// A unit: tokens tok0 .. tok0 + ntok - 1 of a sequence (tile i: n of them). Its
+// depth chunks (128 rows: eight slices) belong to one tile each, but for one
+// that both may share. Where none is shared they come in turns, tile 0's, tile
+// 1's, tile 0's .. : while one tile's softmax runs the other's next product can.
 struct Unit {
     int tok0, ntok;
     int nk;                 // sequence keys its last token sees
     int n_seq, n_items;
     int nkv0, nkv1;         // sequence items tile 0 / 1 takes part in
-    int dhi0, dlo1, dhi1;   // depth items of tile 0: [n_seq, dhi0), of tile 1: [dlo1, dhi1)
+    int pairs;              // leading pairs of depth items in turns
+    int c0_end, c1_begin, chunks;  // chunks of tile 0: [0, c0_end), of tile 1: [c1_begin, chunks)
+    // depth chunk of item n_seq + e, and back
+    __device__ __forceinline__ int chunk(int e) const {
+        return e < 2 * pairs ? (e & 1 ? c1_begin : 0) + (e >> 1) : e - pairs;
+    }
+    __device__ __forceinline__ int item_of(int c) const {
+        if (pairs == 0) return n_seq + c;
+        return n_seq + (c >= c1_begin ? 2 * (c - c1_begin) + 1 : c < pairs ? 2 * c : c + pairs);
+    }
     __device__ __forceinline__ bool part(int i, int x) const {
-        return i ? x < nkv1 || (x >= dlo1 && x < dhi1) : x < nkv0 || (x >= n_seq && x < dhi0);
+        if (x < n_seq) return x < (i ? nkv1 : nkv0);
+        const int c = chunk(x - n_seq);
+        return i ? c >= c1_begin && c < chunks : c < c0_end;
     }
 };
 
@@ -130,10 +146,11 @@ __device__ __forceinline__ Unit make_unit(const PreParams& p, const SeqInfo& s, 
     u.nkv0 = (keys_seen(s, u.tok0 + nv0 - 1, max_keys) + kItemKeys - 1) / kItemKeys;
     u.nkv1 = nv1 ? u.n_seq : 0;
     const int dep0 = nv0 * p.DSL, dep = u.ntok * p.DSL;  // slices
-    u.dhi0 = u.n_seq + (dep0 + kSlices - 1) / kSlices;
-    u.dlo1 = u.n_seq + dep0 / kSlices;
-    u.dhi1 = nv1 ? u.n_seq + (dep + kSlices - 1) / kSlices : u.dlo1;
-    u.n_items = max(u.n_seq + (dep + kSlices - 1) / kSlices, 1);
+    const int chunks = u.chunks = (dep + kSlices - 1) / kSlices;
+    u.c0_end = (dep0 + kSlices - 1) / kSlices;
+    u.c1_begin = nv1 ? dep0 / kSlices : chunks;
+    u.pairs = u.c0_end == u.c1_begin ? chunks - u.c1_begin : 0;  // (tile 1 never has more than tile 0)
+    u.n_items = max(u.n_seq + chunks, 1);
     return u;
 }
 
@@ -190,10 +207,11 @@ __device__ __forceinline__ long long table_keys(const PagedCache& c) {
     return min((long long)c.max_blocks * c.page_size, 0x7fffff00LL);
 }
 
-// The pieces of this CTA's part. Every warp walks them alike, with its own
-// state in shared memory: the loops keep in registers only what they use.
-struct Walk {
-    int b, kvh, rt, first, piece, end, left;
+// A piece of this CTA's part: items [first, end) of a unit. The producer, which
+// is ahead of the others, walks from piece to piece and describes each in a
+// ring of them; walking takes about as long as half an item.
+struct Piece {
+    int b, kvh, rt, first, end, left;  // left: items of the part from here on
     SeqInfo sq;
     Unit u;
     __device__ __forceinline__ void shape(const PreParams& p) {
@@ -204,7 +222,6 @@ struct Walk {
         left -= end - first;
         if (left <= 0) return false;
         first = 0;
-        ++piece;
         if (++rt * 2 * p.n >= sq.n) {
             rt = 0;
             if (++kvh == p.c.Hkv) {
@@ -219,20 +236,70 @@ struct Walk {
     }
 };
 
-static_assert(sizeof(PreBars) + kWalks * sizeof(Walk) <= kCtl && sizeof(PreBars) % 8 == 0, "control block");
+static_assert(sizeof(PreBars) + kPieces * sizeof(Piece) <= kCtl && sizeof(PreBars) % 8 == 0, "control block");
 
-// A warp's step to its next piece: lane 0 walks, everyone sees the result.
-__device__ __forceinline__ bool next_piece(Walk* w, const PreParams& p, int lane) {
-    __syncwarp();
-    bool more = false;
-    if (lane == 0) {
-        Walk v = *w;
-        more = v.next(p);
-        *w = v;
+// softmax_columns for an item of which the row sees columns [lo, hi) less those
+// in `holes` (bit k: columns 16 k ..). In chunks of 32 columns, read twice, in
+// rolled loops: items like this are a few per unit, and the unrolled code of
+// 128 masked columns (26 KB of it) pushed everything else out of the
+// instruction cache wherever units are short.
+__device__ __forceinline__ void softmax_masked(uint32_t tS, uint32_t tO, int lo, int hi, uint32_t holes, float sl2, int it,
+                                               float& m, float& l) {
+    auto load = [&](int c, float (&s)[32]) {
+        uint32_t su[32];
+        ptx::tmem_ld32(tS + c * 32, su);
+        ptx::tmem_wait_ld();
+        const int a = min(max(lo - 32 * c, 0), 32), e = min(max(hi - 32 * c, 0), 32);  // columns [a, e) of the chunk
+        uint32_t vis = (e >= 32 ? 0xffffffffu : (1u << e) - 1u) & ~(a >= 32 ? 0xffffffffu : (1u << a) - 1u);
+        if ((holes >> (2 * c)) & 1) vis &= 0xffff0000u;
+        if ((holes >> (2 * c + 1)) & 1) vis &= 0x0000ffffu;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s[k] = (vis >> k) & 1 ? __uint_as_float(su[k]) : -INFINITY;
+    };
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        float s[32];
+        load(c, s);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) mx = fmaxf(mx, s[k]);
     }
-    more = __shfl_sync(0xffffffffu, more, 0);
-    __syncwarp();
-    return more;
+    const float mxs = mx * sl2;
+    if (__any_sync(0xffffffffu, mxs > m + kRescaleThreshold)) {
+        const float mnew = fmaxf(m, mxs);
+        const float corr = (mnew == -INFINITY) ? 1.f : ptx::ex2(m - mnew);
+        if (it > 0) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                ptx::tmem_ld32(tO + c * 32, o);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                ptx::tmem_st32(tO + c * 32, o);
+            }
+        }
+        l *= corr;
+        m = mnew;
+    }
+    const float ref = (m == -INFINITY) ? 0.f : m;
+    float acc = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        float s[32];
+        load(c, s);
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float p0 = ptx::ex2(fmaf(s[2 * k], sl2, -ref)), p1 = ptx::ex2(fmaf(s[2 * k + 1], sl2, -ref));
+            acc += p0 + p1;
+            pk[k] = ptx::pack_bf16x2(p0, p1);
+        }
+        ptx::tmem_st16(tS + c * 16, pk);  // over columns whose S has been read
+    }
+    ptx::tmem_wait_st();
+    ptx::tc_fence_before();
+    l += acc;
 }
 
 // Sets the non-finite elements of a bf16 value tile to 0. Returns whether this
@@ -286,20 +353,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
     const PagedCache& c = p.c;
     const int cta = blockIdx.x;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
-        ptx::mbar_init(&bars->q_full, 1);
-        ptx::mbar_init(&bars->q_empty, 1);
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(&bars->full[s], 1);
             ptx::mbar_init(&bars->empty[s], 1);
             ptx::mbar_init(&bars->raw_full[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&bars->q_full[i], 1);
+            ptx::mbar_init(&bars->q_empty[i], 1);
             ptx::mbar_init(&bars->s_full[i], 1);
             ptx::mbar_init(&bars->p_full[i], 4);
             ptx::mbar_init(&bars->o_final[i], 1);
             ptx::mbar_init(&bars->o_empty[i], 4);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            ptx::mbar_init(&bars->piece_full[i], 1);
+            ptx::mbar_init(&bars->piece_empty[i], kPieceUsers);
         }
         ptx::mbar_init(&bars->drain, 1);
         for (int i = 0; i < kMeta; ++i) bars->bad_piece[i] = -1;
@@ -309,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
         p.desc[cta] = make_int4(0, 0, 0, 0);
     }
     // ---- the list of items: each thread sums a run of sequences, then a scan
-    Walk* walks = reinterpret_cast<Walk*>(bars + 1);
+    Piece* pieces = reinterpret_cast<Piece*>(bars + 1);
     {
         const long long max_keys = table_keys(c);
         const int per = (c.B + kThreads - 1) / kThreads;
@@ -344,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
         const long long lo = part_begin(total, cta, W), hi = part_begin(total, cta + 1, W);
         long long at = incl - mine * c.Hkv;
         if (lo >= at && lo < incl) {  // one thread: the part begins in its run
-            Walk w;
+            Piece w;
             for (w.b = b0; w.b < b1; ++w.b) {
                 w.sq = seq_info(c, w.b);
                 const long long k = seq_items(p, w.sq, max_keys);
@@ -364,9 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                 at += k * c.Hkv;
             }
             w.left = (int)(hi - lo);
-            w.piece = 0;
             w.shape(p);
-            for (int i = 0; i < kWalks; ++i) walks[i] = w;
+            pieces[0] = w;
             bars->total = total;
             bars->hi = hi;
             bars->W = W;
@@ -375,13 +444,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
     }
     const uint32_t tmem = bars->tmem_base;
     const int n = p.n;
+    // piece k's description, once it is there (nullptr: the wait ran out)
+    auto take_piece = [&](int k) -> const Piece* {
+        const bool got = ptx::mbar_wait(&bars->piece_full[k % kPieces], (k / kPieces) & 1, wait_limit, abort_flag);
+        return got ? pieces + k % kPieces : nullptr;
+    };
 
     if (warp >= 8) ptx::setmaxnreg_dec<kControlRegs>();
     if (warp == kProducerWarp) {
         // -------------------------------------------------------- TMA warp
         int st = 0;
         uint32_t ph = 1, used = 0, full_par = 0, raw_par = 0, last_raw = 0;  // per-stage bits for the drain
-        uint32_t q_par = 0;
+        int q_loads = 0;  // of tiles 0 and 1 in turn
         bool ok = true;
         int item = 0;  // items of the part so far
         if (lane == 0) {
@@ -393,9 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                 ptx::prefetch_tmap(&p.tm_vd);
             }
         }
-        Walk* w = walks + 8;
-        for (bool more = true; more && ok; more = next_piece(w, p, lane)) {
-            const int first = w->first, end = w->end, piece = w->piece, kvh = w->kvh, b = w->b;
+        for (int piece = 0; ok; ++piece) {
+            const Piece* w = pieces + piece % kPieces;
+            if (lane == 0) ptx::mbar_arrive(&bars->piece_full[piece % kPieces]);
+            const int first = w->first, end = w->end, kvh = w->kvh, b = w->b;
             const int n_seq = w->u.n_seq, nk = w->u.nk, ntok = w->u.ntok;
             const int row0 = w->sq.q0 + w->u.tok0, pos_first = w->sq.pos0 + w->u.tok0;
             const int sl0 = first * kSlices;
@@ -443,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                                              pg < 0 ? c.num_pages : pg);
                     } else {
                         const int sl = lane & 7, half = (lane >> 3) & 1;
-                        const int y = (x - n_seq) * kSlices + sl;
+                        const int y = w->u.chunk(x - n_seq) * kSlices + sl;
                         const int tok = p.DSL ? y / p.DSL : 0, s16 = p.DSL ? y % p.DSL : 0;
                         if (lane < 16 && half < p.halves)
                             ptx::tma_load_4d(dst + half * kHalfBytes + sl * 2048, kv ? &p.tm_vd : &p.tm_kd, bar,
@@ -456,24 +531,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                 }
                 if (x == first && ok) {
                     // this piece's queries, once the piece before has used its own
-                    if (piece > 0) {
-                        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bars->q_empty, (piece - 1) & 1, wait_limit, abort_flag))) {
+                    for (int i = 0; i < 2 && ok; ++i) {
+                        if (piece > 0 &&
+                            !__all_sync(0xffffffffu, ptx::mbar_wait(&bars->q_empty[i], (piece - 1) & 1, wait_limit, abort_flag))) {
                             if (lane == 0) flag_timeout(p, bars);
                             ok = false;
                             break;
                         }
+                        if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->q_full[i], p.halves * n * p.G * 128);
+                        __syncwarp();
+                        if (lane < p.halves)
+                            ptx::tma_load_4d(sQ + i * kTileBytes + lane * kHalfBytes, &p.tm_q, &bars->q_full[i], lane * 64,
+                                             kvh * p.G, row0 + i * n, 0);
+                        ++q_loads;
                     }
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->q_full, 2 * p.halves * n * p.G * 128);
-                    __syncwarp();
-                    if (lane < 4 && (lane & 1) < p.halves)
-                        ptx::tma_load_4d(sQ + (lane >> 1) * kTileBytes + (lane & 1) * kHalfBytes, &p.tm_q, &bars->q_full,
-                                 (lane & 1) * 64, kvh * p.G, row0 + (lane >> 1) * n, 0);
-                    q_par = piece + 1;  // query loads issued
                 }
             }
+            // describe the next piece
+            if (!ok || w->left <= end - first) break;
+            const int nx = (piece + 1) % kPieces;
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&bars->piece_empty[nx], (((piece + 1) / kPieces) & 1) ^ 1, wait_limit,
+                                                        abort_flag))) {
+                if (lane == 0) flag_timeout(p, bars);
+                break;
+            }
+            if (lane == 0) {
+                Piece v = *w;
+                v.next(p);
+                pieces[nx] = v;
+            }
+            __syncwarp();
         }
         // every load this CTA issued lands before it exits
-        if (q_par) ptx::mbar_wait(&bars->q_full, (q_par - 1) & 1, kNoPollLimit, nullptr);
+        for (int i = 0; i < 2; ++i)
+            if (q_loads > i) ptx::mbar_wait(&bars->q_full[i], ((q_loads - 1 - i) / 2) & 1, kNoPollLimit, nullptr);
         for (int s = 0; s < kStages; ++s) {
             if (!((used >> s) & 1)) continue;
             if ((last_raw >> s) & 1) ptx::mbar_wait(&bars->raw_full[s], ((raw_par >> s) & 1) ^ 1, kNoPollLimit, nullptr);
@@ -512,7 +603,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                 }
                 ptx::mma_commit(&bars->s_full[i]);
             };
-            uint32_t pp0 = 0, pp1 = 0;       // p_full phases
+            auto issue_pv = [&](int i, uint64_t vd, bool add) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    ptx::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, vd + (uint64_t)(k * 128), idesc_pv,
+                                (add || k > 0) ? 1u : 0u);
+            };
+            uint32_t pp = 0;                 // p_full phases, a bit per tile
             int st = 0;
             uint32_t ph = 0;
             auto advance = [&]() {
@@ -522,24 +619,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                 }
             };
             bool ok = true;
-            Walk* w = walks + 9;
-            for (bool more = true; more && ok; more = w->next(p)) {
+            bool more = true;
+            for (int piece = 0; more && ok; ++piece) {
+                const Piece* w = take_piece(piece);
+                if (!w) {
+                    flag_timeout(p, bars);
+                    break;
+                }
                 const Unit u = w->u;
-                const int first = w->first, end = w->end, piece = w->piece;
-                ok = wait_all(&bars->q_full, piece & 1);
-                if (!ok) break;
-                ok = wait_all(&bars->full[st], ph);
-                if (!ok) break;
-                if (u.part(0, first)) issue_s(0, st);
-                if (u.part(1, first)) issue_s(1, st);
-                ptx::mma_commit(&bars->empty[st]);
-                advance();
-                int cnt0 = 0, cnt1 = 0;      // items of this piece each tile has taken part in
-                // the last one of each (first - 1: none): its O is final there
-                const int last0 = min(end, u.dhi0) > max(first, u.n_seq) ? min(end, u.dhi0) - 1
-                                                                         : max(min(end, u.nkv0), first) - 1;
-                const int last1 = min(end, u.dhi1) > max(first, u.dlo1) ? min(end, u.dhi1) - 1
-                                                                        : max(min(end, u.nkv1), first) - 1;
+                const int first = w->first, end = w->end;
+                more = w->left > end - first;
+                ptx::mbar_arrive(&bars->piece_empty[piece % kPieces]);
+                // the last item of each tile in the piece (first - 1: none)
+                int last0 = end - 1, last1 = u.ntok > n ? end - 1 : first - 1;
+                while (last0 >= first && !u.part(0, last0)) --last0;
+                while (last1 >= first && !u.part(1, last1)) --last1;
+                // Rolled forms for the items at a piece's ends (the instruction
+                // cache again); `who` bits: the tiles that take part
+                auto issue_tail = [&](int i, int x, int slot) {
+                    const uint64_t kd_ = k0 + (uint64_t)slot * kSlotUnits, qd_ = q0 + (uint64_t)i * kSlotUnits;
+#pragma unroll 1
+                    for (int k = 0; k < 4 * p.halves; ++k) {
+                        const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
+                        ptx::mma_ss(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0);
+                    }
+                    ptx::mma_commit(&bars->s_full[i]);
+                    // after its last product the tile's queries may go
+                    if (x == (i ? last1 : last0)) ptx::mma_commit(&bars->q_empty[i]);
+                };
                 // o_final may run at most one piece ahead of either tile's warps,
                 // also of a tile that takes no part in these pieces
                 auto finish = [&](int i) {
@@ -547,47 +654,86 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                     ptx::mma_commit(&bars->o_final[i]);
                     return true;
                 };
-                if (last0 < first) ok = finish(0);
-                if (ok && last1 < first) ok = finish(1);
-                for (int x = first; x < end && ok; ++x) {
+                auto who = [&](int x) { return (u.part(0, x) ? 1u : 0u) | (u.part(1, x) ? 2u : 0u); };
+                uint32_t cur = who(first), started = 0;
+                ok = wait_all(&bars->full[st], ph);
+#pragma unroll 1
+                for (int i = 0; i < 2 && ok; ++i) {
+                    ok = wait_all(&bars->q_full[i], piece & 1);
+                    if (!ok) break;
+                    if ((cur >> i) & 1) issue_tail(i, first, st);
+                    if ((i ? last1 : last0) < first) {
+                        ptx::mma_commit(&bars->q_empty[i]);
+                        ok = finish(i);
+                    }
+                }
+                if (!ok) break;
+                ptx::mma_commit(&bars->empty[st]);
+                advance();
+                // Items that both tiles take part in, as in the next one, and that
+                // are nobody's last: the loop that has to keep the tensor core fed
+                const int plain = min(end - 2, min(u.nkv0, u.nkv1) - 2);
+                int x = first;
+                for (; x < plain; ++x) {
+                    const int st_v = st;
+                    if (!(ok = wait_all(&bars->full[st], ph))) break;
+                    advance();
+                    const uint64_t vd = v0 + (uint64_t)st_v * kSlotUnits;
+                    if (!(ok = wait_all(&bars->p_full[0], pp & 1))) break;
+                    issue_pv(0, vd, x > first);
+                    if (!(ok = wait_all(&bars->full[st], ph))) break;
+                    issue_s(0, st);
+                    if (!(ok = wait_all(&bars->p_full[1], pp >> 1))) break;
+                    issue_pv(1, vd, x > first);
+                    issue_s(1, st);
+                    ptx::mma_commit(&bars->empty[st_v]);
+                    ptx::mma_commit(&bars->empty[st]);
+                    advance();
+                    pp ^= 3;
+                    started = 3;
+                }
+                if (x > first) cur = 3;
+                for (; x < end && ok; ++x) {
                     const int st_v = st;
                     ok = wait_all(&bars->full[st], ph);
                     if (!ok) break;
                     advance();
                     const bool next = x + 1 < end;
                     const uint64_t vd = v0 + (uint64_t)st_v * kSlotUnits;
+                    const uint32_t nxt = next ? who(x + 1) : 0u;
                     bool k_ready = false;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (!ok) break;
-                        if (u.part(i, x)) {
-                            const int cnt = i ? cnt1 : cnt0;
+                    // round 0: a tile that sits this item out can go ahead with the
+                    // next; then tile 0's and tile 1's P V and next S
+#pragma unroll 1
+                    for (int step = 0; step < 4 && ok; ++step) {
+                        const int i = step & 1;
+                        const bool in = (cur >> i) & 1;
+                        if (step < 2 ? in : !in) continue;
+                        if (in) {
                             // (P also says that this tile's warps have read the O of the
                             // piece before, which the piece's first P V overwrites)
-                            if (!wait_all(&bars->p_full[i], i ? pp1 : pp0)) {
+                            if (!wait_all(&bars->p_full[i], (pp >> i) & 1)) {
                                 ok = false;
                                 break;
                             }
-                            if (i) pp1 ^= 1; else pp0 ^= 1;
-#pragma unroll
+                            pp ^= 1u << i;
+#pragma unroll 1
                             for (int k = 0; k < 8; ++k)
                                 ptx::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, vd + (uint64_t)(k * 128), idesc_pv,
-                                            (cnt > 0 || k > 0) ? 1u : 0u);
-                            if (i) ++cnt1; else ++cnt0;
+                                            ((started >> i) & 1) | (k > 0 ? 1u : 0u));
+                            started |= 1u << i;
                             if (x == (i ? last1 : last0) && !finish(i)) {
                                 ok = false;
                                 break;
                             }
                         }
-                        if (next && u.part(i, x + 1)) {
-                            if (!k_ready) {
-                                if (!wait_all(&bars->full[st], ph)) {
-                                    ok = false;
-                                    break;
-                                }
-                                k_ready = true;
+                        if ((nxt >> i) & 1) {
+                            if (!k_ready && !wait_all(&bars->full[st], ph)) {
+                                ok = false;
+                                break;
                             }
-                            issue_s(i, st);
+                            k_ready = true;
+                            issue_tail(i, x + 1, st);
                         }
                     }
                     if (!ok) break;
@@ -596,8 +742,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                         ptx::mma_commit(&bars->empty[st]);
                         advance();
                     }
+                    cur = nxt;
                 }
-                if (ok) ptx::mma_commit(&bars->q_empty);
             }
             ptx::mma_commit(&bars->drain);
             ptx::mbar_wait(&bars->drain, 0, kNoPollLimit, nullptr);
@@ -609,11 +755,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
         int st = 0;
         uint32_t raw_par = 0;
         bool ok = true;
-        Walk* w = walks + warp;
-        for (bool more = true; more && ok; more = next_piece(w, p, lane)) {
-            const int end = w->end, piece = w->piece, n_seq = w->u.n_seq, nk = w->u.nk;
+        bool more = true;
+        for (int piece = 0; more && ok; ++piece) {
+            const Piece* w = take_piece(piece);
+            if (!ptx::bar_and(1, kCond, w != nullptr)) {
+                if (ct == 0) flag_timeout(p, bars);
+                break;
+            }
+            const int first = w->first, end = w->end, n_seq = w->u.n_seq, nk = w->u.nk;
             const int pos_first = w->sq.pos0 + w->u.tok0;
-            for (int x = w->first; x < end && ok; ++x) {
+            more = w->left > end - first;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars->piece_empty[piece % kPieces]);
+            for (int x = first; x < end && ok; ++x) {
                 const bool seq = x < n_seq;
                 for (int kv = 0; kv < 2 && ok; ++kv) {
                     uint8_t* slot = sRing + st * kTileBytes;
@@ -649,16 +803,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
         bool ok = true;
         uint32_t sp = 0;                      // s_full phase
         int item = 0;
-        Walk* w = walks + warp;
-        for (bool more = true; more && ok; more = next_piece(w, p, lane)) {
-            const int first = w->first, end = w->end, piece = w->piece, n_seq = w->u.n_seq;
+        bool more = true;
+        for (int piece = 0; more && ok; ++piece) {
+            const Piece* w = take_piece(piece);
+            if (!__all_sync(0xffffffffu, w != nullptr)) {
+                if (lane == 0) flag_timeout(p, bars);
+                break;
+            }
+            const int first = w->first, end = w->end, n_seq = w->u.n_seq;
+            more = w->left > end - first;
             const int pos = used ? w->sq.pos0 + w->u.tok0 + tl : -1;
             float m = -INFINITY, l = 0.f;
             int it = 0;
-            // this tile's items: sequence items below nkv, depth items [dlo, dhi)
-            const int nkv = i ? w->u.nkv1 : w->u.nkv0, dlo = i ? w->u.dlo1 : n_seq, dhi = i ? w->u.dhi1 : w->u.dhi0;
+            const int nkv = i ? w->u.nkv1 : w->u.nkv0;
             for (int x = first; x < end; ++x, ++item) {
-                if (!(x < nkv || (x >= dlo && x < dhi))) continue;
+                if (x < n_seq ? x >= nkv : !w->u.part(i, x)) continue;
                 const bool got = ptx::mbar_wait(&bars->s_full[i], sp, wait_limit, abort_flag);
                 if (!__all_sync(0xffffffffu, got)) {
                     if (lane == 0) flag_timeout(p, bars);
@@ -670,29 +829,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                 const bool seq = x < n_seq;
                 const int kbase = x * kItemKeys;
                 const uint32_t holes = bars->holes[item % kMeta];
-                softmax_columns(
-                    tS, tO,
-                    [&](float (&s)[128]) {
-                        if (seq) {
-                            if (kbase + 127 > pos) {
-#pragma unroll
-                                for (int k = 0; k < 128; ++k)
-                                    if (kbase + k > pos) s[k] = -INFINITY;
-                            }
-                            if (holes) {
-#pragma unroll
-                                for (int k = 0; k < 128; ++k)
-                                    if ((holes >> (k >> 4)) & 1) s[k] = -INFINITY;
-                            }
-                        } else {
-                            uint32_t vis[4];
-                            depth_col_mask((tl * p.DSL - (x - n_seq) * kSlices) * 16, p.Ld, false, 0ull, vis);
-#pragma unroll
-                            for (int k = 0; k < 128; ++k)
-                                if (!((vis[k >> 5] >> (k & 31)) & 1u)) s[k] = -INFINITY;
-                        }
-                    },
-                    p.sl2, it, m, l);
+                // the columns this row sees
+                int lo = 0, hi = pos - kbase + 1;
+                if (!seq) {
+                    lo = (tl * p.DSL - w->u.chunk(x - n_seq) * kSlices) * 16;
+                    hi = lo + p.Ld;
+                }
+                if (__all_sync(0xffffffffu, seq && hi >= 128) && !holes)
+                    softmax_columns(tS, tO, [](float (&)[128]) {}, p.sl2, it, m, l);
+                else
+                    softmax_masked(tS, tO, lo, hi, holes, p.sl2, it, m, l);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&bars->p_full[i]);
                 ++it;
@@ -742,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                         }
                     }
                     for (int s = 0; s < p.Ld; ++s) {
-                        const int xi = n_seq + (tl * p.DSL + s / 16) / kSlices;
+                        const int xi = w->u.item_of((tl * p.DSL + s / 16) / kSlices);
                         if (xi >= first && xi < end)
                             add(p.vd + (((long long)(w->sq.q0 + w->u.tok0 + tl) * p.Ld_cap + s) * c.Hkv + kvh) * c.d);
                     }
@@ -778,12 +924,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
             // O has been read
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars->o_empty[i]);
+            if (lane == 0) {
+                ptx::mbar_arrive(&bars->o_empty[i]);
+                ptx::mbar_arrive(&bars->piece_empty[piece % kPieces]);
+            }
         }
     }
 
     ptx::tc_fence_before();
     __syncthreads();
+    // the join may be scheduled once every CTA is about here; earlier its
+    // waiting blocks would take issue slots from this kernel (QQ)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
