@@ -383,84 +383,107 @@ __device__ __forceinline__ int code_of(float x, float inv) {
     return y == y ? (int)fminf(fmaxf(rintf(y), -127.f), 127.f) : 0;
 }
 
+// The codes of VEC values. Without non-finite ones among them (`odd`) no code
+// is out of range, and adding 1.5 * 2^23 rounds x / scale to a whole number,
+// half to even, in the sum's low byte: x * inv is exact, so the fused add rounds
+// once.
 template <int VEC>
-__device__ __forceinline__ void store_codes(int8_t* dst, const float (&x)[VEC], float inv) {
-    Chunk<int8_t, VEC> o;
+__device__ __forceinline__ void store_codes(int8_t* dst, const float (&x)[VEC], float inv, bool odd) {
+    if (odd || VEC < 4) {
+        Chunk<int8_t, VEC> o;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) o.x[e] = (int8_t)code_of(x[e], inv);
-    *reinterpret_cast<Chunk<int8_t, VEC>*>(dst) = o;
+        for (int e = 0; e < VEC; ++e) o.x[e] = (int8_t)code_of(x[e], inv);
+        *reinterpret_cast<Chunk<int8_t, VEC>*>(dst) = o;
+        return;
+    }
+    uint32_t w[VEC >= 4 ? VEC / 4 : 1];
+#pragma unroll
+    for (int e = 0; e + 3 < VEC; e += 4) {
+        uint32_t b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b[k] = __float_as_uint(__fmaf_rn(x[e + k], inv, 12582912.f));
+        w[e / 4] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    }
+    if (VEC == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[VEC / 8]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
 }
 
 // One CTA: the rows of one page that start at token i (the first token of its
-// sequence or of a page), for one kv-head, keys (kv = 0) or values.
+// sequence or of a page), for one kv-head: the first half of its threads the
+// keys (kv = 0), the second the values. Two passes, the largest value and the
+// codes; the second finds the rows in L1. The loops stay rolled: a run is a few
+// rounds, and unrolled the code took longer to fetch than to run.
+constexpr int kRunThreads = 128;  // of each half
+
 template <typename T, int VEC, bool INTER>
-__device__ __forceinline__ void page_run(const AppendArgs& a, int i, const Token& t, int g, int kv, float* red) {
+__device__ __forceinline__ void page_run(const AppendArgs& a, int i, const Token& t, int g, float* red) {
     const PagedCache& c = a.c;
-    const int P = c.page_size, d = c.d, tid = threadIdx.x;
+    const int P = c.page_size, d = c.d, kv = threadIdx.x / kRunThreads, tid = threadIdx.x % kRunThreads;
     const int page = page_of(c, t.b, t.pos / P);
     const int r0 = (int)(t.pos % P);
+    float* scales = (kv ? a.v_scale : a.k_scale) + (long long)max(page, 0) * c.Hkv + g;
+    const float old = r0 && page >= 0 ? *scales : 0.f;
     long long rows = min((long long)__ldg(c.cu_q + t.b + 1), (long long)c.N) - i;
     if (rows > P - r0) rows = P - r0;
     if (a.rope && rows > a.rope_len - t.pos) rows = a.rope_len - t.pos;
     const int rot = (kv == 0 && a.rope) ? a.rot : 0;
-    const Units n(d, rot, INTER, VEC);
+    Units n(d, rot, INTER, VEC);
+    // rows without a rotation: two chunks a unit as well, where they are even
+    const bool pairs = rot == 0 && d % (2 * VEC) == 0;
+    if (pairs) n.total = d / (2 * VEC);
     const T* src = kv ? static_cast<const T*>(a.v) + (long long)g * d : static_cast<const T*>(a.k) + (long long)g * d;
     const long long ss = kv ? a.sv : a.sk;
     T* dep = static_cast<T*>(kv ? a.vd : a.kd);
     const int total = (int)rows * n.total;
-    // kHold units a thread at a time, all loads before the first use; a run that
-    // fits keeps them for the second pass
-    constexpr int kHold = 4, kGroup = kHold * kWarps * 32;
-    Chunk<T, VEC> ca[kHold], cb[kHold];
-    Unit<VEC, INTER> un;
-    auto load = [&](int x0) {
-#pragma unroll
-        for (int j = 0; j < kHold; ++j) {
-            const int x = x0 + j * kWarps * 32 + tid;
-            if (x >= total) break;
-            un.place(x % n.total, n, rot);
-            un.load(src + (i + x / n.total) * ss, ca[j], cb[j]);
-        }
-    };
-    auto each = [&](int x0, auto&& use) {  // use(row of the run, p, q)
-#pragma unroll
-        for (int j = 0; j < kHold; ++j) {
-            const int x = x0 + j * kWarps * 32 + tid;
-            if (x >= total) break;
-            const int r = x / n.total;
-            un.set(x % n.total, n, rot, rot ? a.rope + (t.pos + r) * a.rot : nullptr);
+    auto each = [&](auto&& use) {  // use(row of the run, unit, p, q) for every unit of every row
+#pragma unroll 1
+        for (int x = tid; x < total; x += kRunThreads) {
+            const int r = x / n.total, u = x - r * n.total;
+            Unit<VEC, INTER> un;
+            un.set(u, n, rot, rot ? a.rope + (t.pos + r) * a.rot : nullptr);
+            if (pairs) {
+                un.f0 = u * VEC;
+                un.f1 = un.f0 + d / 2;
+                un.two = true;
+            }
+            Chunk<T, VEC> ca, cb;
+            un.load(src + (i + r) * ss, ca, cb);
             float p[VEC], q[VEC];
-            un.turn(ca[j], cb[j], p, q);
-            use(r, p, q);
+            un.turn(ca, cb, p, q);
+            use(r, un, p, q);
         }
     };
-    float amax = 0.f;
-    for (int x0 = 0; x0 < total; x0 += kGroup) {
-        load(x0);
-        each(x0, [&](int r, const float (&p)[VEC], const float (&q)[VEC]) {
-            if (dep) un.store(dep + (((long long)(i + r) * a.Ld + a.slot) * c.Hkv + g) * d, p, q);
+    float amax = 0.f, none = 0.f;  // none: 0 * every value, NaN when one is not finite
+    each([&](int r, const Unit<VEC, INTER>& un, const float (&p)[VEC], const float (&q)[VEC]) {
+        if (dep) un.store(dep + (((long long)(i + r) * a.Ld + a.slot) * c.Hkv + g) * d, p, q);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, finite_abs(p[e]));
-            if (un.two)
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, finite_abs(q[e]));
+        for (int e = 0; e < VEC; ++e) {  // (q is 0 where a unit has one part)
+            amax = fmaxf(amax, fmaxf(fabsf(p[e]), fabsf(q[e])));
+            none = fmaf(p[e], 0.f, fmaf(q[e], 0.f, none));
+        }
+    });
+    if (page < 0) return;  // uniform over the CTA
+    const bool odd = __syncthreads_or(!(none == 0.f));
+    if (odd) {  // the largest finite value
+        amax = 0.f;
+        each([&](int, const Unit<VEC, INTER>&, const float (&p)[VEC], const float (&q)[VEC]) {
+#pragma unroll 1
+            for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fmaxf(finite_abs(p[e]), finite_abs(q[e])));
         });
     }
-    if (page < 0) return;  // uniform over the CTA
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    float* scales = (kv ? a.v_scale : a.k_scale) + (long long)page * c.Hkv + g;
-    const float old = r0 ? *scales : 0.f;
-    if (tid % 32 == 0) red[tid / 32] = amax;
+    if (tid % 32 == 0) red[threadIdx.x / 32] = amax;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, red[w]);
+    for (int w = 0; w < kRunThreads / 32; ++w) amax = fmaxf(amax, red[kv * (kRunThreads / 32) + w]);
     const float now = fmaxf(old, scale_for(amax));
     const float inv = now > 0.f ? 1.f / now : 0.f;  // exact: a power of two
     int8_t* codes = static_cast<int8_t*>(kv ? a.v_pages : a.k_pages) + ((long long)page * c.Hkv + g) * P * d;
     if (r0 && old != now) {
         const float ratio = __fmul_rn(old, inv);
-        for (int x = tid; x < r0 * (d / VEC); x += kWarps * 32) {
+#pragma unroll 1
+        for (int x = tid; x < r0 * (d / VEC); x += kRunThreads) {
             Chunk<int8_t, VEC>* at = reinterpret_cast<Chunk<int8_t, VEC>*>(codes + (long long)x * VEC);
             Chunk<int8_t, VEC> ch = *at;
 #pragma unroll
@@ -468,35 +491,32 @@ __device__ __forceinline__ void page_run(const AppendArgs& a, int i, const Token
             *at = ch;
         }
     }
-    for (int x0 = 0; x0 < total; x0 += kGroup) {
-        if (total > kGroup) load(x0);
-        each(x0, [&](int r, const float (&p)[VEC], const float (&q)[VEC]) {
-            int8_t* dst = codes + (long long)(r0 + r) * d;
-            store_codes<VEC>(dst + un.f0, p, inv);
-            if (un.two) store_codes<VEC>(dst + un.f1, q, inv);
-        });
-    }
+    each([&](int r, const Unit<VEC, INTER>& un, const float (&p)[VEC], const float (&q)[VEC]) {
+        int8_t* dst = codes + (long long)(r0 + r) * d;
+        store_codes<VEC>(dst + un.f0, p, inv, odd);
+        if (un.two) store_codes<VEC>(dst + un.f1, q, inv, odd);
+    });
     __syncthreads();  // everyone has read the old scale and `red`
     if (tid == 0) *scales = now;
 }
 
 // Blocks [0, q_blocks): q heads of the tokens, one warp per share. The rest:
 // block x serves the page runs that start in tokens [chunk*x', chunk*(x'+1))
-// for one (kv-head, keys or values).
-template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32)
+// for one kv-head. Without Q (no queries, or the bulk form takes them) the code
+// for them does not hold registers, and three CTAs fit an SM instead of one.
+template <typename T, int VEC, bool INTER, bool Q>
+__global__ void __launch_bounds__(2 * kRunThreads, Q ? 1 : 3)
 paged_append_q8_kernel(const AppendArgs a, int shares, int q_blocks, int chunk) {
-    if ((int)blockIdx.x < q_blocks) {
-        const long long w = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
+    if (Q && (int)blockIdx.x < q_blocks) {
+        const long long w = (long long)blockIdx.x * (2 * kRunThreads / 32) + threadIdx.x / 32;
         if (w / shares >= a.c.N) return;
         const int per = (a.Hq + shares - 1) / shares, h0 = (int)(w % shares) * per;
         if (h0 < a.Hq) token_heads<T, VEC, INTER>(a, (int)(w / shares), h0, min(h0 + per, a.Hq));
         return;
     }
-    __shared__ float red[kWarps];
-    const int jobs = 2 * a.c.Hkv, x = blockIdx.x - q_blocks;
-    const int job = x % jobs;
-    const long long i0 = (long long)(x / jobs) * chunk;
+    __shared__ float red[2 * kRunThreads / 32];
+    const int x = blockIdx.x - q_blocks, g = x % a.c.Hkv;
+    const long long i0 = (long long)(x / a.c.Hkv) * chunk;
     // lane e looks at token i0 + e. A run starts where the sequence's new
     // tokens start (counting from the first one with a position) and at each
     // page's first row.
@@ -523,7 +543,7 @@ paged_append_q8_kernel(const AppendArgs a, int shares, int q_blocks, int chunk) 
         run.b = __shfl_sync(0xffffffffu, t.b, e);
         run.pos = __shfl_sync(0xffffffffu, t.pos, e);
         run.taken = true;
-        page_run<T, VEC, INTER>(a, (int)i0 + e, run, job >> 1, job & 1, red);
+        page_run<T, VEC, INTER>(a, (int)i0 + e, run, g, red);
     }
 }
 
@@ -574,12 +594,13 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
     } else {
         // tokens whose page runs a CTA serves: one while the CTAs fit the GPU
         // about at once (every CTA looks up its tokens first), a page at most
-        const long long waves = (long long)c.N * 2 * c.Hkv / (148 * 8);
+        const long long waves = (long long)c.N * c.Hkv / (148 * 4);
         const int chunk = (int)std::max(1LL, std::min<long long>(waves, std::min(c.page_size, 32)));
-        const long long q_blocks = a.q && !bulk ? blocks : 0;
-        const long long all = q_blocks + ((long long)c.N + chunk - 1) / chunk * 2 * c.Hkv;
+        const long long q_blocks = a.q && !bulk ? ((long long)c.N * shares + 7) / 8 : 0;
+        const long long all = q_blocks + ((long long)c.N + chunk - 1) / chunk * c.Hkv;
         if (all > 0x7fffffffLL) return cudaErrorInvalidValue;
-        paged_append_q8_kernel<T, VEC, INTER><<<(unsigned)all, kWarps * 32, 0, s>>>(a, shares, (int)q_blocks, chunk);
+        if (q_blocks) paged_append_q8_kernel<T, VEC, INTER, true><<<(unsigned)all, 2 * kRunThreads, 0, s>>>(a, shares, (int)q_blocks, chunk);
+        else paged_append_q8_kernel<T, VEC, INTER, false><<<(unsigned)all, 2 * kRunThreads, 0, s>>>(a, shares, 0, chunk);
     }
     return cudaGetLastError();
 }
