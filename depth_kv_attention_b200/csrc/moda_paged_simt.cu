@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "paged_common.cuh"
 
@@ -22,6 +23,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kDMax = 128;
 constexpr int kMaxWarps = 16;
+constexpr int kKeys = 2;  // keys a lane group has in flight
 
 template <typename T>
 struct alignas(sizeof(T) * 4) Four {
@@ -30,27 +32,38 @@ struct alignas(sizeof(T) * 4) Four {
 
 // Features 32c + 4l .. +3 of a row, c = 0..3 (zero past d; d % 4 == 0).
 template <typename T>
-__device__ __forceinline__ void load16(const T* row, int d, int l, float (&x)[16]) {
+__device__ __forceinline__ void load16(const T* row, int d, int l, T (&x)[16]) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int f = 32 * c + 4 * l;
-        Four<T> v;
+        Four<T> v{};
         if (f < d) v = *reinterpret_cast<const Four<T>*>(row + f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[4 * c + e] = f < d ? pg_to_f(v.x[e]) : 0.f;
+        for (int e = 0; e < 4; ++e) x[4 * c + e] = v.x[e];
     }
 }
 
 struct State {
     float m, l, o[16];
-    // One key with logit s (log2 domain) and values v.
-    __device__ __forceinline__ void add(float s, const float (&v)[16]) {
-        const float mn = fmaxf(m, s);
-        const float ref = mn == -INFINITY ? 0.f : mn;
-        const float corr = exp2f(m - ref), p = exp2f(s - ref);
-        l = l * corr + p;
+    // Keys with logits s (log2 domain) and values v times sv; a logit of -inf
+    // adds nothing (its values are zeros then).
+    template <typename KV>
+    __device__ __forceinline__ void add(const float (&s)[kKeys], const KV (&v)[kKeys][16], const float (&sv)[kKeys]) {
+        float mn = m;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = fmaf(o[e], corr, p * v[e]);
+        for (int u = 0; u < kKeys; ++u) mn = fmaxf(mn, s[u]);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float corr = exp2f(m - ref);
+        l *= corr;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] *= corr;
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            const float p = exp2f(s[u] - ref), pv = p * sv[u];
+            l += p;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(pv, pg_to_f(v[u][e]), o[e]);
+        }
         m = mn;
     }
     __device__ __forceinline__ void join_lanes(int mask) {
@@ -75,7 +88,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_fwd_simt_kernel(const Pa
     const long long pos = (long long)__ldg(c.ctx_lens + b) - ((long long)__ldg(c.cu_q + b + 1) - i);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
     const int grp = warp * 4 + lane / 8, groups = warps * 4, l8 = lane % 8;
-    float q[16];
+    T q[16];
     load16(static_cast<const T*>(a.q) + ((long long)i * a.Hq + h) * d, d, l8, q);
     const float sl2 = a.scale * kLog2e;
     State st;
@@ -83,39 +96,65 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_fwd_simt_kernel(const Pa
     st.l = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) st.o[e] = 0.f;
-    auto dot = [&](const float (&k)[16]) {
-        float s = 0.f;
+    // One step: keys `on` says, their rows at k + at[u] and v + at[u].
+    auto step = [&](const auto* k, const auto* v, const long long (&at)[kKeys], const bool (&on)[kKeys],
+                    const float (&ks)[kKeys], const float (&vs)[kKeys]) {
+        using KT = std::remove_cv_t<std::remove_pointer_t<decltype(k)>>;
+        KT kx[kKeys][16] = {}, vx[kKeys][16] = {};
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s = fmaf(q[e], k[e], s);
+        for (int u = 0; u < kKeys; ++u)
+            if (on[u]) load16(k + at[u], d, l8, kx[u]);
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u)
+            if (on[u]) load16(v + at[u], d, l8, vx[u]);
+        float s[kKeys];
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            s[u] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[u] = fmaf(pg_to_f(q[e]), pg_to_f(kx[u][e]), s[u]);
+        }
         // the eight lanes of a key take part together (their loop bounds are equal)
         const unsigned lanes = 0xffu << (lane & 24);
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(lanes, s, o);
-        return s * sl2;
-    };
-    const long long nk = min(pos + 1, (long long)c.max_blocks * P);
-    for (long long j = grp; j < nk; j += groups) {
-        const int page = page_of(c, b, j / P);
-        if (page < 0) continue;
-        const long long hrow = (long long)page * c.Hkv + g, at = (hrow * P + j % P) * d;
-        float k[16], v[16];
-        load16(static_cast<const KV*>(a.k_pages) + at, d, l8, k);
-        load16(static_cast<const KV*>(a.v_pages) + at, d, l8, v);
-        float s = dot(k);
-        if (a.k_scale) {
-            s *= __ldg(a.k_scale + hrow);
-            const float sv = __ldg(a.v_scale + hrow);
+        for (int o = 1; o < 8; o <<= 1)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] *= sv;
+            for (int u = 0; u < kKeys; ++u) s[u] += __shfl_xor_sync(lanes, s[u], o);
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) s[u] = on[u] ? s[u] * ks[u] : -INFINITY;
+        st.add(s, vx, vs);
+    };
+    long long at[kKeys];
+    bool on[kKeys];
+    float ks[kKeys], vs[kKeys];
+    // positions are below 2^31, steps of kKeys * groups <= 128 keep j below 2^32
+    const unsigned nk = (unsigned)max(0LL, min(pos + 1, (long long)c.max_blocks * P));
+    for (unsigned j = grp; j < nk; j += kKeys * groups) {
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            const unsigned ju = j + u * groups, blk = ju / (unsigned)P;
+            const int page = ju < nk ? page_of(c, b, blk) : -1;
+            const long long hrow = (long long)max(page, 0) * c.Hkv + g;
+            on[u] = page >= 0;
+            at[u] = (hrow * P + (ju - blk * P)) * d;
+            ks[u] = sl2;
+            vs[u] = 1.f;
+            if (a.k_scale && on[u]) {
+                ks[u] *= __ldg(a.k_scale + hrow);
+                vs[u] = __ldg(a.v_scale + hrow);
+            }
         }
-        st.add(s, v);
+        step(static_cast<const KV*>(a.k_pages), static_cast<const KV*>(a.v_pages), at, on, ks, vs);
     }
-    for (int x = grp; x < a.Ld; x += groups) {
-        const long long at = (((long long)i * a.Ld_cap + x) * c.Hkv + g) * d;
-        float k[16], v[16];
-        load16(static_cast<const T*>(a.kd) + at, d, l8, k);
-        load16(static_cast<const T*>(a.vd) + at, d, l8, v);
-        st.add(dot(k), v);
+    for (int x = grp; x < a.Ld; x += kKeys * groups) {
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            on[u] = x + u * groups < a.Ld;
+            at[u] = (((long long)i * a.Ld_cap + x + u * groups) * c.Hkv + g) * d;
+            ks[u] = sl2;
+            vs[u] = 1.f;
+        }
+        step(static_cast<const T*>(a.kd), static_cast<const T*>(a.vd), at, on, ks, vs);
     }
     __syncwarp();
     st.join_lanes(8);
