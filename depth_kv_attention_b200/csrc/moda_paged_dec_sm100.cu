@@ -38,6 +38,7 @@
 //    cores and clear them before the product.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -934,8 +935,6 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-constexpr int kWholeKeys = 512;
-
 // Query rows of a unit by the rows a sequence has: 8, 16, 32 or 64.
 int rows_of(int max_q, int G) {
     const long long r = (long long)max_q * G;
@@ -985,9 +984,17 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
     p.lse = a.lse;
     p.Hq = a.Hq; p.G = a.G; p.Ld = a.Ld; p.DSL = (a.Ld + kSliceRows - 1) / kSliceRows;
     p.W = C::kParts;
-    // the longest unit the block table allows, in stages: short ones stay whole
-    // and save the join
-    p.split = (long long)c.max_blocks * c.page_size + (long long)a.Ld * ((C::MR + a.G - 2) / a.G + 1) > kWholeKeys;
+    // The longest unit that the block table allows, in stages. Up to two stay
+    // whole and save the join (one sequence of 16 tokens, G = 4: 8.6 us against
+    // 9.4). Longer ones are cut to use the idle CTAs (one of 256 tokens: 9.8
+    // against 12.0; 64 rows of one kv-head 12.6 against 18.6), up to six stages
+    // only when there are units for a share of the CTAs anyway (64 sequences of
+    // 128, four tokens each: 33.1 cut, 23.8 whole).
+    const long long keys = (long long)c.max_blocks * c.page_size;
+    const long long toks = std::min((C::MR + a.G - 2) / a.G + 1, a.max_q);
+    const long long stages = (keys + C::KEYS - 1) / C::KEYS + (toks * p.DSL + C::DS - 1) / C::DS;
+    const long long units = (long long)c.B * c.Hkv * (((long long)a.max_q * a.G + C::MR - 1) / C::MR);
+    p.split = stages > 6 || (stages > 2 && stages * C::kParts > 10 * units);
     p.sl2 = a.scale * 1.4426950408889634f;
     p.status = a.status;
     p.wait_limit = a.wait_limit;
