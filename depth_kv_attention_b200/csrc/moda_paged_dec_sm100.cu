@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
                 // parts up to the one that holds the unit's last stage
                 const long long last = hi - left + u.st - 1;  // its index in the list (this piece starts at hi - left)
                 const int c_last = (int)(((last + 1) * W + total - 1) / total) - 1;
-                p.desc[cta] = make_int4(b, kvh, rt, (c_last - cta + 1) | u.rows << 16);
+                p.desc[cta] = make_int4(sq.q0, kvh, rt, (c_last - cta + 1) | u.rows << 16);
             }
         }
         left -= end - first;

@@ -245,22 +245,26 @@ static_assert(sizeof(PreBars) + kPieces * sizeof(Piece) <= kCtl && sizeof(PreBar
 // instruction cache wherever units are short.
 __device__ __forceinline__ void softmax_masked(uint32_t tS, uint32_t tO, int lo, int hi, uint32_t holes, float sl2, int it,
                                                float& m, float& l) {
+    // (chunks no row of the warp sees are skipped: of a depth item the 32 / G
+    // tokens of a warp see a part, of a diagonal one the first columns)
     auto load = [&](int c, float (&s)[32]) {
-        uint32_t su[32];
-        ptx::tmem_ld32(tS + c * 32, su);
-        ptx::tmem_wait_ld();
         const int a = min(max(lo - 32 * c, 0), 32), e = min(max(hi - 32 * c, 0), 32);  // columns [a, e) of the chunk
         uint32_t vis = (e >= 32 ? 0xffffffffu : (1u << e) - 1u) & ~(a >= 32 ? 0xffffffffu : (1u << a) - 1u);
         if ((holes >> (2 * c)) & 1) vis &= 0xffff0000u;
         if ((holes >> (2 * c + 1)) & 1) vis &= 0x0000ffffu;
+        if (!__any_sync(0xffffffffu, vis != 0)) return false;
+        uint32_t su[32];
+        ptx::tmem_ld32(tS + c * 32, su);
+        ptx::tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 32; ++k) s[k] = (vis >> k) & 1 ? __uint_as_float(su[k]) : -INFINITY;
+        return true;
     };
     float mx = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         float s[32];
-        load(c, s);
+        if (!load(c, s)) continue;
 #pragma unroll
         for (int k = 0; k < 32; ++k) mx = fmaxf(mx, s[k]);
     }
@@ -287,13 +291,14 @@ __device__ __forceinline__ void softmax_masked(uint32_t tS, uint32_t tO, int lo,
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         float s[32];
-        load(c, s);
-        uint32_t pk[16];
+        uint32_t pk[16] = {};
+        if (load(c, s)) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float p0 = ptx::ex2(fmaf(s[2 * k], sl2, -ref)), p1 = ptx::ex2(fmaf(s[2 * k + 1], sl2, -ref));
-            acc += p0 + p1;
-            pk[k] = ptx::pack_bf16x2(p0, p1);
+            for (int k = 0; k < 16; ++k) {
+                const float p0 = ptx::ex2(fmaf(s[2 * k], sl2, -ref)), p1 = ptx::ex2(fmaf(s[2 * k + 1], sl2, -ref));
+                acc += p0 + p1;
+                pk[k] = ptx::pack_bf16x2(p0, p1);
+            }
         }
         ptx::tmem_st16(tS + c * 16, pk);  // over columns whose S has been read
     }
@@ -914,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                     // parts of the unit, up to the one that holds its last item
                     const long long last = bars->hi - w->left + w->u.n_items;
                     const int c_last = (int)((last * bars->W + bars->total - 1) / bars->total) - 1;
-                    p.desc[cta] = make_int4(w->b, kvh, w->rt, (c_last - cta + 1) | (w->u.ntok <= n ? w->u.ntok * p.G : 128 + (w->u.ntok - n) * p.G) << 16);
+                    p.desc[cta] = make_int4(w->sq.q0, kvh, w->rt, (c_last - cta + 1) | (w->u.ntok <= n ? w->u.ntok * p.G : 128 + (w->u.ntok - n) * p.G) << 16);
                 }
                 if (!whole)
                     *reinterpret_cast<float2*>(p.part_ml + ((long long)ps * kRows + i * 128 + r) * 2) = make_float2(m, l);

@@ -17,7 +17,7 @@ struct JoinParams {
     float* lse;
     const float* part_o;   // [2W][MR][D]: CTA x's first part in 2x, its last (the start of a unit) in 2x + 1
     const float* part_ml;  // [2W][MR][2]
-    const int4* desc;      // [W]: {sequence, kv-head, tile, parts | rows << 16}, 0: no unit is cut there
+    const int4* desc;      // [W]: {first row of the sequence, kv-head, tile, parts | rows << 16}, 0: no unit is cut there
     int Hq, G;
     int n;  // tokens of a 128-row tile (rows past n G unused), or 0: rows are (token, head) without gaps
 };
@@ -34,9 +34,19 @@ __device__ __forceinline__ int join_passes(const int4& ds) {
     return parts == 0 ? 0 : parts > kShareParts ? rows : (rows + kJoinWarps - 1) / kJoinWarps;
 }
 
+// Parts a warp loads at a time, and blocks per SM. A pass is a chain of loads
+// (about 1.5 us), so what counts is how many are under way: two parts are the
+// rule where units are large and cut once, and batches of four leave room for
+// four blocks (148 units of 256 rows: 28 us with two blocks and batches of
+// eight). Decode units may have hundreds of parts.
+template <int MR>
+struct JoinCfg {
+    static constexpr int kBatch = MR == 256 ? 4 : 8, kBlocks = MR == 256 ? 4 : 2;
+};
+
 template <int MR, int D, int W>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const JoinParams p) {
-    constexpr int E = D / 32;
+__global__ void __launch_bounds__(kJoinWarps * 32, JoinCfg<MR>::kBlocks) paged_join_kernel(const JoinParams p) {
+    constexpr int E = D / 32, kBatch = JoinCfg<MR>::kBatch;
     __shared__ int sums[kJoinWarps], ends[W];
     __shared__ int4 descs[W];
     __shared__ float sml[kJoinWarps][2], so[kJoinWarps][D];
@@ -69,12 +79,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const JoinP
     __syncthreads();
     const int all = ends[W - 1];
     for (int item = blockIdx.x; item < all; item += gridDim.x) {
-        int lo = 0, hi = W - 1;  // first CTA whose running sum passes the item
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (ends[mid] <= item) lo = mid + 1; else hi = mid;
-        }
-        const int x = lo;
+        int x = 0;  // first CTA whose running sum passes the item
+#pragma unroll
+        for (int w = 0; w < W; w += 32)
+            x += __popc(__ballot_sync(0xffffffffu, w + lane < W && ends[min(w + lane, W - 1)] <= item));
         const int4 ds = descs[x];
         const int parts = ds.w & 0xffff, rows = ds.w >> 16;
         const int pass = item - (x ? ends[x - 1] : 0);
@@ -85,13 +93,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const JoinP
         const int tok = p.n ? (2 * ds.z + (r >> 7)) * p.n + rr / p.G : rr / p.G;
         const bool there = r < rows && (!p.n || rr < p.n * p.G);
         auto slot = [&](int i) { return (long long)(i == 0 ? 2 * x + 1 : 2 * (x + i)) * MR + r; };
-        const SeqInfo sq = seq_info(p.c, ds.x);
         float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
         if (there) {
-            // eight parts at a time, all loads in flight together
-            constexpr int kBatch = 8;
+            // all loads of a batch in flight together
             const int step = shared ? kJoinWarps : 1;
             for (int i0 = shared ? warp : 0; i0 < parts; i0 += kBatch * step) {
                 float2 ml[kBatch];
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const JoinP
         }
         if (there && (!shared || warp == 0)) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const long long orow = (long long)(sq.q0 + tok) * p.Hq + ds.y * p.G + rr % p.G;
+            const long long orow = (long long)(ds.x + tok) * p.Hq + ds.y * p.G + rr % p.G;
 #pragma unroll
             for (int e = 0; e < E; e += 2)
                 if (lane * E + e < p.c.d)
@@ -175,7 +181,7 @@ cudaError_t launch_paged_join(const JoinParams& p, cudaStream_t s) {
     // launched while the attention drains; waits for its end on the device
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(2 * 148);
+    cfg.gridDim = dim3(JoinCfg<MR>::kBlocks * 148);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
