@@ -77,8 +77,8 @@ struct PreParams {
 constexpr int kThreads = 384;
 constexpr int kCondFirst = 10;
 constexpr int kCond = 64;        // conditioning threads
-constexpr int kSoftmaxRegs = 216;
-constexpr int kControlRegs = 72;
+constexpr int kSoftmaxRegs = 200;
+constexpr int kControlRegs = 104;
 constexpr int kStages = 5;
 
 struct __align__(8) PreBars {
@@ -577,8 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------ MMA thread
-        if (lane == 0) {
+        // ------------------------------------------------------ MMA warp -
+        {
+            const uint32_t lead = lane == 0;
             constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, kItemKeys, 0, 0);
             const uint32_t idesc_pv = ptx::idesc_bf16_f32(128, p.halves * 64, 0, 1);
             const bool two_halves = p.halves == 2;
@@ -587,13 +588,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
             const uint64_t k0 = ptx::umma_desc_sw128(sRa, 16, 1024);
             const uint64_t v0 = ptx::umma_desc_sw128(sRa, kHalfBytes, 1024);
             constexpr uint64_t kSlotUnits = kTileBytes >> 4;
-            auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+            auto wait_one = [&](uint64_t* bar, uint32_t parity) {
                 const bool got = ptx::mbar_wait(bar, parity, wait_limit, abort_flag);
-                if (!got) flag_timeout(p, bars);
-                else ptx::tc_fence_after();
+                if (got) ptx::tc_fence_after();
+                else flag_timeout(p, bars);
                 return got;
             };
-            auto issue_s = [&](int i, int st) {
+            auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+                const bool got = __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, wait_limit, abort_flag));
+                if (got) ptx::tc_fence_after();
+                else if (lead) flag_timeout(p, bars);
+                return got;
+            };
+            auto issue_s_one = [&](int i, int st) {
                 const uint64_t kd_ = k0 + (uint64_t)st * kSlotUnits, qd_ = q0 + (uint64_t)i * kSlotUnits;
                 // both halves of the features, or the first alone
                 if (two_halves) {
@@ -608,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                 }
                 ptx::mma_commit(&bars->s_full[i]);
             };
-            auto issue_pv = [&](int i, uint64_t vd, bool add) {
+            auto issue_pv_one = [&](int i, uint64_t vd, bool add) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     ptx::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, vd + (uint64_t)(k * 128), idesc_pv,
@@ -627,14 +634,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
             bool more = true;
             for (int piece = 0; more && ok; ++piece) {
                 const Piece* w = take_piece(piece);
-                if (!w) {
-                    flag_timeout(p, bars);
+                if (!__all_sync(0xffffffffu, w != nullptr)) {
+                    if (lead) flag_timeout(p, bars);
                     break;
                 }
                 const Unit u = w->u;
                 const int first = w->first, end = w->end;
                 more = w->left > end - first;
-                ptx::mbar_arrive(&bars->piece_empty[piece % kPieces]);
+                __syncwarp();
+                if (lead) ptx::mbar_arrive(&bars->piece_empty[piece % kPieces]);
                 // the last item of each tile in the piece (first - 1: none)
                 int last0 = end - 1, last1 = u.ntok > n ? end - 1 : first - 1;
                 while (last0 >= first && !u.part(0, last0)) --last0;
@@ -646,17 +654,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
 #pragma unroll 1
                     for (int k = 0; k < 4 * p.halves; ++k) {
                         const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
-                        ptx::mma_ss(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0);
+                        ptx::mma_ss_lead(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0, lead);
                     }
-                    ptx::mma_commit(&bars->s_full[i]);
+                    ptx::mma_commit_lead(&bars->s_full[i], lead);
                     // after its last product the tile's queries may go
-                    if (x == (i ? last1 : last0)) ptx::mma_commit(&bars->q_empty[i]);
+                    if (x == (i ? last1 : last0)) ptx::mma_commit_lead(&bars->q_empty[i], lead);
                 };
                 // o_final may run at most one piece ahead of either tile's warps,
                 // also of a tile that takes no part in these pieces
                 auto finish = [&](int i) {
                     if (piece > 0 && !wait_all(&bars->o_empty[i], (piece - 1) & 1)) return false;
-                    ptx::mma_commit(&bars->o_final[i]);
+                    ptx::mma_commit_lead(&bars->o_final[i], lead);
                     return true;
                 };
                 auto who = [&](int x) { return (u.part(0, x) ? 1u : 0u) | (u.part(1, x) ? 2u : 0u); };
@@ -668,35 +676,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                     if (!ok) break;
                     if ((cur >> i) & 1) issue_tail(i, first, st);
                     if ((i ? last1 : last0) < first) {
-                        ptx::mma_commit(&bars->q_empty[i]);
+                        ptx::mma_commit_lead(&bars->q_empty[i], lead);
                         ok = finish(i);
                     }
                 }
                 if (!ok) break;
-                ptx::mma_commit(&bars->empty[st]);
+                ptx::mma_commit_lead(&bars->empty[st], lead);
                 advance();
                 // Items that both tiles take part in, as in the next one, and that
                 // are nobody's last: the loop that has to keep the tensor core fed
                 const int plain = min(end - 2, min(u.nkv0, u.nkv1) - 2);
                 int x = first;
+                if (lead) {
                 for (; x < plain; ++x) {
                     const int st_v = st;
-                    if (!(ok = wait_all(&bars->full[st], ph))) break;
+                    if (!(ok = wait_one(&bars->full[st], ph))) break;
                     advance();
                     const uint64_t vd = v0 + (uint64_t)st_v * kSlotUnits;
-                    if (!(ok = wait_all(&bars->p_full[0], pp & 1))) break;
-                    issue_pv(0, vd, x > first);
-                    if (!(ok = wait_all(&bars->full[st], ph))) break;
-                    issue_s(0, st);
-                    if (!(ok = wait_all(&bars->p_full[1], pp >> 1))) break;
-                    issue_pv(1, vd, x > first);
-                    issue_s(1, st);
+                    if (!(ok = wait_one(&bars->p_full[0], pp & 1))) break;
+                    issue_pv_one(0, vd, x > first);
+                    if (!(ok = wait_one(&bars->full[st], ph))) break;
+                    issue_s_one(0, st);
+                    if (!(ok = wait_one(&bars->p_full[1], pp >> 1))) break;
+                    issue_pv_one(1, vd, x > first);
+                    issue_s_one(1, st);
                     ptx::mma_commit(&bars->empty[st_v]);
                     ptx::mma_commit(&bars->empty[st]);
                     advance();
                     pp ^= 3;
                     started = 3;
                 }
+                }
+                __syncwarp();
+                x = __shfl_sync(0xffffffffu, x, 0);
+                st = __shfl_sync(0xffffffffu, st, 0);
+                ph = __shfl_sync(0xffffffffu, ph, 0);
+                pp = __shfl_sync(0xffffffffu, pp, 0);
+                started = __shfl_sync(0xffffffffu, started, 0);
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0);
                 if (x > first) cur = 3;
                 for (; x < end && ok; ++x) {
                     const int st_v = st;
@@ -724,8 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                             pp ^= 1u << i;
 #pragma unroll 1
                             for (int k = 0; k < 8; ++k)
-                                ptx::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, vd + (uint64_t)(k * 128), idesc_pv,
-                                            ((started >> i) & 1) | (k > 0 ? 1u : 0u));
+                                ptx::mma_ts_lead(tmem + 256 + i * 128, tmem + i * 128 + k * 8, vd + (uint64_t)(k * 128), idesc_pv,
+                                            ((started >> i) & 1) | (k > 0 ? 1u : 0u), lead);
                             started |= 1u << i;
                             if (x == (i ? last1 : last0) && !finish(i)) {
                                 ok = false;
@@ -742,15 +759,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                         }
                     }
                     if (!ok) break;
-                    ptx::mma_commit(&bars->empty[st_v]);
+                    ptx::mma_commit_lead(&bars->empty[st_v], lead);
                     if (next) {
-                        ptx::mma_commit(&bars->empty[st]);
+                        ptx::mma_commit_lead(&bars->empty[st], lead);
                         advance();
                     }
                     cur = nxt;
                 }
             }
-            ptx::mma_commit(&bars->drain);
+            ptx::mma_commit_lead(&bars->drain, lead);
             ptx::mbar_wait(&bars->drain, 0, kNoPollLimit, nullptr);
         }
         __syncwarp();
