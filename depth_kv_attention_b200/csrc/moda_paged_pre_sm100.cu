@@ -533,23 +533,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                         st = 0;
                         ph ^= 1;
                     }
-                }
-                if (x == first && ok) {
-                    // this piece's queries, once the piece before has used its own
-                    for (int i = 0; i < 2 && ok; ++i) {
-                        if (piece > 0 &&
-                            !__all_sync(0xffffffffu, ptx::mbar_wait(&bars->q_empty[i], (piece - 1) & 1, wait_limit, abort_flag))) {
-                            if (lane == 0) flag_timeout(p, bars);
-                            ok = false;
-                            break;
+                    if (kv == 0 && x == first && ok) {
+                        // this piece's queries, once the piece before has used its own
+                        for (int i = 0; i < 2 && ok; ++i) {
+                            if (piece > 0 &&
+                                !__all_sync(0xffffffffu, ptx::mbar_wait(&bars->q_empty[i], (piece - 1) & 1, wait_limit, abort_flag))) {
+                                if (lane == 0) flag_timeout(p, bars);
+                                ok = false;
+                                break;
+                            }
+                            if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->q_full[i], p.halves * n * p.G * 128);
+                            __syncwarp();
+                            if (lane < p.halves)
+                                ptx::tma_load_4d(sQ + i * kTileBytes + lane * kHalfBytes, &p.tm_q, &bars->q_full[i], lane * 64,
+                                                 kvh * p.G, row0 + i * n, 0);
+                            ++q_loads;
                         }
-                        if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->q_full[i], p.halves * n * p.G * 128);
-                        __syncwarp();
-                        if (lane < p.halves)
-                            ptx::tma_load_4d(sQ + i * kTileBytes + lane * kHalfBytes, &p.tm_q, &bars->q_full[i], lane * 64,
-                                             kvh * p.G, row0 + i * n, 0);
-                        ++q_loads;
                     }
+                    if (!ok) break;
                 }
             }
             // describe the next piece
