@@ -64,7 +64,6 @@ struct PreParams {
     int4* desc;
     int Hq, G, n, Ld, Ld_cap, DSL;  // a tile has n tokens, n * G of its 128 rows
     int lg_step;                    // 2n = 1 << lg_step <= 128, or -1
-    int halves;                     // 64-feature halves of a row in use
     int box_rows;  // rows of a page box: the largest power of two that divides the page size, at most 128
     float sl2;
     unsigned int* status;
@@ -346,6 +345,8 @@ __device__ __forceinline__ bool clear_nonfinite(uint8_t* slot, int ct, int rows,
     return met;
 }
 
+// HALVES: 64-feature halves of a row in use.
+template <int HALVES>
 __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_constant__ PreParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -510,13 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                     used |= bit;
                     if (kv == 0 && lane == 0) bars->holes[item % kMeta] = seq ? none : 0;
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, p.halves * kHalfBytes);
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, HALVES * kHalfBytes);
                     __syncwarp();
                     if (seq) {
                         // boxes of box_rows rows and half of the features
                         const int half = lane & 1, r0 = (lane >> 1) * p.box_rows;
                         const int pg = __shfl_sync(0xffffffffu, page, ((rel & 31) + (r0 >> 4)) & 31);
-                        if (r0 < kItemKeys && half < p.halves)
+                        if (r0 < kItemKeys && half < HALVES)
                             // a page that is not there lies outside the map: zeros
                             ptx::tma_load_4d(dst + half * kHalfBytes + r0 * 128, kv ? &p.tm_v : &p.tm_k, bar, half * 64,
                                              pg < 0 ? 0 : (x * kItemKeys + r0) % c.page_size, kvh,
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                         const int sl = lane & 7, half = (lane >> 3) & 1;
                         const int y = w->u.chunk(x - n_seq) * kSlices + sl;
                         const int tok = p.DSL ? y / p.DSL : 0, s16 = p.DSL ? y % p.DSL : 0;
-                        if (lane < 16 && half < p.halves)
+                        if (lane < 16 && half < HALVES)
                             ptx::tma_load_4d(dst + half * kHalfBytes + sl * 2048, kv ? &p.tm_vd : &p.tm_kd, bar,
                                              half * 64, kvh, s16 * 16, p.DSL && tok < ntok ? row0 + tok : c.N);
                     }
@@ -542,9 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                                 ok = false;
                                 break;
                             }
-                            if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->q_full[i], p.halves * n * p.G * 128);
+                            if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->q_full[i], HALVES * n * p.G * 128);
                             __syncwarp();
-                            if (lane < p.halves)
+                            if (lane < HALVES)
                                 ptx::tma_load_4d(sQ + i * kTileBytes + lane * kHalfBytes, &p.tm_q, &bars->q_full[i], lane * 64,
                                                  kvh * p.G, row0 + i * n, 0);
                             ++q_loads;
@@ -582,8 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
         {
             const uint32_t lead = lane == 0;
             constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, kItemKeys, 0, 0);
-            const uint32_t idesc_pv = ptx::idesc_bf16_f32(128, p.halves * 64, 0, 1);
-            const bool two_halves = p.halves == 2;
+            constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HALVES * 64, 0, 1);
             const uint32_t sQa = ptx::smem_u32(sQ), sRa = ptx::smem_u32(sRing);
             const uint64_t q0 = ptx::umma_desc_sw128(sQa, 16, 1024);
             const uint64_t k0 = ptx::umma_desc_sw128(sRa, 16, 1024);
@@ -603,16 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
             };
             auto issue_s_one = [&](int i, int st) {
                 const uint64_t kd_ = k0 + (uint64_t)st * kSlotUnits, qd_ = q0 + (uint64_t)i * kSlotUnits;
-                // both halves of the features, or the first alone
-                if (two_halves) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
-                        ptx::mma_ss(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0);
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) ptx::mma_ss(tmem + i * 128, qd_ + k * 2, kd_ + k * 2, idesc_qk, k > 0);
+                for (int k = 0; k < 4 * HALVES; ++k) {
+                    const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
+                    ptx::mma_ss(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0);
                 }
                 ptx::mma_commit(&bars->s_full[i]);
             };
@@ -653,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                 auto issue_tail = [&](int i, int x, int slot) {
                     const uint64_t kd_ = k0 + (uint64_t)slot * kSlotUnits, qd_ = q0 + (uint64_t)i * kSlotUnits;
 #pragma unroll 1
-                    for (int k = 0; k < 4 * p.halves; ++k) {
+                    for (int k = 0; k < 4 * HALVES; ++k) {
                         const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
                         ptx::mma_ss_lead(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0, lead);
                     }
@@ -694,13 +688,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                     if (!(ok = wait_one(&bars->full[st], ph))) break;
                     advance();
                     const uint64_t vd = v0 + (uint64_t)st_v * kSlotUnits;
-                    if (!(ok = wait_one(&bars->p_full[0], pp & 1))) break;
-                    issue_pv_one(0, vd, x > first);
-                    if (!(ok = wait_one(&bars->full[st], ph))) break;
-                    issue_s_one(0, st);
-                    if (!(ok = wait_one(&bars->p_full[1], pp >> 1))) break;
-                    issue_pv_one(1, vd, x > first);
-                    issue_s_one(1, st);
+#pragma unroll 1
+                    for (int i = 0; i < 2 && ok; ++i) {
+                        if (!(ok = wait_one(&bars->p_full[i], (pp >> i) & 1))) break;
+                        issue_pv_one(i, vd, x > first);
+                        if (i == 0 && !(ok = wait_one(&bars->full[st], ph))) break;
+                        issue_s_one(i, st);
+                    }
+                    if (!ok) break;
                     ptx::mma_commit(&bars->empty[st_v]);
                     ptx::mma_commit(&bars->empty[st]);
                     advance();
@@ -804,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                             break;
                         }
                         const int rows = seq ? min(nk - x * kItemKeys, kItemKeys) : kItemKeys;
-                        if (clear_nonfinite(slot, ct, rows, p.halves)) bars->bad_piece[piece % kMeta] = piece;
+                        if (clear_nonfinite(slot, ct, rows, HALVES)) bars->bad_piece[piece % kMeta] = piece;
                         ptx::fence_proxy_async_smem();
                         ptx::bar_sync(1, kCond);
                         if (ct == 0) ptx::mbar_arrive(full);
@@ -965,7 +960,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
     }
 }
 
-cudaError_t launch(const PagedFwdArgs& a, char* ws, cudaStream_t s) {
+template <int HALVES>
+cudaError_t launch_halves(const PagedFwdArgs& a, char* ws, cudaStream_t s) {
     PreParams p;
     memset(static_cast<void*>(&p), 0, sizeof(p));
     const PagedCache& c = a.c;
@@ -974,7 +970,6 @@ cudaError_t launch(const PagedFwdArgs& a, char* ws, cudaStream_t s) {
     p.lg_step = -1;
     for (int lg = 1; lg <= 7; ++lg)
         if (2 * p.n == 1 << lg) p.lg_step = lg;
-    p.halves = c.d <= 64 ? 1 : 2;
     const cuuint64_t d = c.d;
     {
         const cuuint64_t dims[4] = {d, (cuuint64_t)a.Hq, (cuuint64_t)c.N, 1};
@@ -1014,13 +1009,18 @@ cudaError_t launch(const PagedFwdArgs& a, char* ws, cudaStream_t s) {
     p.part_ml = reinterpret_cast<float*>(ws + kParts * sizeof(int4));
     p.part_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(p.part_ml + (size_t)2 * kParts * kRows * 2) + 31) & ~uintptr_t(31));
     static SmemLimit limit;
-    cudaError_t err = limit.raise(reinterpret_cast<const void*>(paged_pre_kernel), kSmemBytes);
+    const auto kern = paged_pre_kernel<HALVES>;
+    cudaError_t err = limit.raise(reinterpret_cast<const void*>(kern), kSmemBytes);
     if (err != cudaSuccess) return err;
-    paged_pre_kernel<<<kParts, kThreads, kSmemBytes, s>>>(p);
+    kern<<<kParts, kThreads, kSmemBytes, s>>>(p);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     JoinParams j{p.c, p.out, p.lse, p.part_o, p.part_ml, p.desc, p.Hq, p.G, p.n};
     return launch_paged_join<kRows, kD, kParts>(j, s);
+}
+
+cudaError_t launch(const PagedFwdArgs& a, char* ws, cudaStream_t s) {
+    return a.c.d <= 64 ? launch_halves<1>(a, ws, s) : launch_halves<2>(a, ws, s);
 }
 
 // 8-bit pages to bf16 pages of the same numbering, for the pages this call
