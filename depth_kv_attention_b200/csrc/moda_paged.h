@@ -72,8 +72,11 @@ cudaError_t launch_paged_dec(const PagedFwdArgs& a, cudaStream_t s);
 bool paged_pre_supported(const PagedFwdArgs& a);
 size_t paged_pre_workspace(int Hkv, int d, long long num_pages, int page_size, bool q8);
 cudaError_t launch_paged_pre(const PagedFwdArgs& a, cudaStream_t s);
-// Rows per sequence and kv-head from which it is the one that runs.
-constexpr int kPagedPreRows = 65;
+// Rows per sequence and kv-head from which it is the one that runs. 48
+// sequences of 3000 tokens, 33 to 40 rows: G = 8 78 us against 116 on the other
+// kernel, G = 1 166 against 320, 8-bit pages 290 against 442; at 32 rows 78
+// against 75 and, on 8-bit pages, 143 against 93.
+constexpr int kPagedPreRows = 33;
 // Every shape (moda_paged_simt.cu).
 cudaError_t launch_paged_fwd_simt(const PagedFwdArgs& a, cudaStream_t s);
 

@@ -7,20 +7,21 @@
 //
 // What bounds it: a token's G rows share every key, so a step reads K and V
 // once and does 4 G d operations per key and head: memory-bound up to about
-// G * tokens = 64. The design keeps loads in flight and everything else out of
+// G * tokens = 64. (From 33 rows on the tcgen05 kernel is the faster one, so
+// this one has tiles of up to 32.) The design keeps loads in flight and everything else out of
 // the way:
-//  * The stages of all units (paged_units.cuh) are cut into equal parts, two
-//    CTAs per SM; cut units leave (m, l, O) in the workspace and a small
+//  * The stages of all units (paged_units.cuh) are cut into equal parts, two or
+//    three CTAs per SM; cut units leave (m, l, O) in the workspace and a small
 //    second kernel joins them in a fixed order.
-//  * One producer warp fills a ring of 64-key K and V slots by TMA, one box of
+//  * One producer warp fills a ring of K and V slots (64 or 128 keys) by TMA, one box of
 //    16 rows per page slice, so any page size that is a multiple of 16 works;
 //    page ids and scales are fetched 32 slices at a time, one batch ahead.
 //  * The products are mma.sync m16n8k16 with the KEYS as the 16 rows (S^T = K Q^T,
 //    O^T = V^T P^T): query rows then come in eights, which is what a decode step
 //    has (G heads of a token), where a tcgen05 tile would be 128 rows high. Four
 //    consumer warps, each with its own keys of a stage and its own softmax state,
-//    joined at the unit's end; with 32 or 64 rows two or four of them take 16
-//    rows each of the same keys. Up to 8 rows three CTAs fit an SM, else two. P^T is
+//    joined at the unit's end; with 32 rows two of them take 16 rows each of the
+//    same keys. Up to 8 rows three CTAs fit an SM, else two. P^T is
 //    what the second product wants as its B operand, once its 8 x 8 blocks are
 //    transposed between lanes (movmatrix).
 //  * 8-bit pages: a lane reads whole 16-byte pieces of a row and turns codes
@@ -63,7 +64,7 @@ struct DecParams {
     float* lse;
     float* part_o;   // [2W][MR][D]
     float* part_ml;  // [2W][MR][2]
-    int4* desc;      // [W]: {sequence, kv-head, tile, parts | rows << 16}, 0: no unit is cut there
+    int4* desc;      // [W]: as in JoinParams
     int Hq, G, Ld, DSL, W;
     int split;       // units may be cut (else each stays with one CTA)
     float sl2;
@@ -85,7 +86,7 @@ struct Cfg {
     static constexpr int kThreads = 32 * (kWarps + 1);
     static constexpr int MR = 8 * NR * WR;
     static constexpr int WK = kWarps / WR;                   // warps that share a stage's keys
-    static constexpr int SL = WR == 4 ? 4 : WR == 2 || Q8 ? 2 : 1;  // slices of a stage per warp
+    static constexpr int SL = WR == 2 || Q8 ? 2 : 1;  // slices of a stage per warp
     static constexpr int SPS = SL * WK;                      // slices of a stage
     static constexpr int KEYS = 16 * SPS;
     static constexpr int kSeqSlice = Q8 ? 2048 : 2048 * NH;  // bytes of 16 keys
@@ -935,10 +936,10 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Query rows of a unit by the rows a sequence has: 8, 16, 32 or 64.
+// Query rows of a unit by the rows a sequence has: 8, 16 or 32.
 int rows_of(int max_q, int G) {
     const long long r = (long long)max_q * G;
-    return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : 64;
+    return r <= 8 ? 8 : r <= 16 ? 16 : 32;
 }
 
 bool encode(CUtensorMap* m, bool u8, const void* base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
@@ -1018,8 +1019,7 @@ cudaError_t by_rows(const PagedFwdArgs& a, cudaStream_t s) {
     switch (rows_of(a.max_q, a.G)) {
         case 8: return launch<Q8, NH, 1, 1>(a, s);
         case 16: return launch<Q8, NH, 2, 1>(a, s);
-        case 32: return launch<Q8, NH, 2, 2>(a, s);
-        default: return launch<Q8, NH, 2, 4>(a, s);
+        default: return launch<Q8, NH, 2, 2>(a, s);
     }
 }
 
