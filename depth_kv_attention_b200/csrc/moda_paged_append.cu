@@ -411,8 +411,9 @@ __device__ __forceinline__ void store_codes(int8_t* dst, const float (&x)[VEC], 
 // One CTA: the rows of one page that start at token i (the first token of its
 // sequence or of a page), for one kv-head: the first half of its threads the
 // keys (kv = 0), the second the values. Two passes, the largest value and the
-// codes; the second finds the rows in L1. The loops stay rolled: a run is a few
-// rounds, and unrolled the code took longer to fetch than to run.
+// codes; the second finds the rows in L1. The loops stay rolled, and the passes
+// share one body: a run is a few rounds, and unrolled the code took longer to
+// fetch than to run.
 constexpr int kRunThreads = 128;  // of each half
 
 template <typename T, int VEC, bool INTER>
@@ -435,7 +436,34 @@ __device__ __forceinline__ void page_run(const AppendArgs& a, int i, const Token
     const long long ss = kv ? a.sv : a.sk;
     T* dep = static_cast<T*>(kv ? a.vd : a.kd);
     const int total = (int)rows * n.total;
-    auto each = [&](auto&& use) {  // use(row of the run, unit, p, q) for every unit of every row
+    int8_t* codes = static_cast<int8_t*>(kv ? a.v_pages : a.k_pages) + ((long long)max(page, 0) * c.Hkv + g) * P * d;
+    float amax = 0.f, none = 0.f;  // none: 0 * every value, NaN when one is not finite
+    float now = old, inv = 0.f;
+    bool odd = false;
+    // pass 0: the largest value; 1: the largest finite one, where some are not; 2: the codes
+#pragma unroll 1
+    for (int pass = 0; pass < 3; pass += pass || odd ? 1 : 2) {
+        if (pass == 2) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            if (tid % 32 == 0) red[threadIdx.x / 32] = amax;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kRunThreads / 32; ++w) amax = fmaxf(amax, red[kv * (kRunThreads / 32) + w]);
+            now = fmaxf(old, scale_for(amax));
+            inv = now > 0.f ? 1.f / now : 0.f;  // exact: a power of two
+            if (r0 && old != now) {
+                const float ratio = __fmul_rn(old, inv);
+#pragma unroll 1
+                for (int x = tid; x < r0 * (d / VEC); x += kRunThreads) {
+                    Chunk<int8_t, VEC>* at = reinterpret_cast<Chunk<int8_t, VEC>*>(codes + (long long)x * VEC);
+                    Chunk<int8_t, VEC> ch = *at;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) ch.x[e] = (int8_t)code_of((float)ch.x[e], ratio);
+                    *at = ch;
+                }
+            }
+        }
 #pragma unroll 1
         for (int x = tid; x < total; x += kRunThreads) {
             const int r = x / n.total, u = x - r * n.total;
@@ -448,54 +476,30 @@ __device__ __forceinline__ void page_run(const AppendArgs& a, int i, const Token
             }
             Chunk<T, VEC> ca, cb;
             un.load(src + (i + r) * ss, ca, cb);
-            float p[VEC], q[VEC];
+            float p[VEC], q[VEC];  // (q is 0 where a unit has one part)
             un.turn(ca, cb, p, q);
-            use(r, un, p, q);
+            if (pass == 0) {
+                if (dep) un.store(dep + (((long long)(i + r) * a.Ld + a.slot) * c.Hkv + g) * d, p, q);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    amax = fmaxf(amax, fmaxf(fabsf(p[e]), fabsf(q[e])));
+                    none = fmaf(p[e], 0.f, fmaf(q[e], 0.f, none));
+                }
+            } else if (pass == 1) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fmaxf(finite_abs(p[e]), finite_abs(q[e])));
+            } else {
+                int8_t* dst = codes + (long long)(r0 + r) * d;
+                store_codes<VEC>(dst + un.f0, p, inv, odd);
+                if (un.two) store_codes<VEC>(dst + un.f1, q, inv, odd);
+            }
         }
-    };
-    float amax = 0.f, none = 0.f;  // none: 0 * every value, NaN when one is not finite
-    each([&](int r, const Unit<VEC, INTER>& un, const float (&p)[VEC], const float (&q)[VEC]) {
-        if (dep) un.store(dep + (((long long)(i + r) * a.Ld + a.slot) * c.Hkv + g) * d, p, q);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {  // (q is 0 where a unit has one part)
-            amax = fmaxf(amax, fmaxf(fabsf(p[e]), fabsf(q[e])));
-            none = fmaf(p[e], 0.f, fmaf(q[e], 0.f, none));
-        }
-    });
-    if (page < 0) return;  // uniform over the CTA
-    const bool odd = __syncthreads_or(!(none == 0.f));
-    if (odd) {  // the largest finite value
-        amax = 0.f;
-        each([&](int, const Unit<VEC, INTER>&, const float (&p)[VEC], const float (&q)[VEC]) {
-#pragma unroll 1
-            for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fmaxf(finite_abs(p[e]), finite_abs(q[e])));
-        });
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (tid % 32 == 0) red[threadIdx.x / 32] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kRunThreads / 32; ++w) amax = fmaxf(amax, red[kv * (kRunThreads / 32) + w]);
-    const float now = fmaxf(old, scale_for(amax));
-    const float inv = now > 0.f ? 1.f / now : 0.f;  // exact: a power of two
-    int8_t* codes = static_cast<int8_t*>(kv ? a.v_pages : a.k_pages) + ((long long)page * c.Hkv + g) * P * d;
-    if (r0 && old != now) {
-        const float ratio = __fmul_rn(old, inv);
-#pragma unroll 1
-        for (int x = tid; x < r0 * (d / VEC); x += kRunThreads) {
-            Chunk<int8_t, VEC>* at = reinterpret_cast<Chunk<int8_t, VEC>*>(codes + (long long)x * VEC);
-            Chunk<int8_t, VEC> ch = *at;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) ch.x[e] = (int8_t)code_of((float)ch.x[e], ratio);
-            *at = ch;
+        if (pass == 0) {
+            if (page < 0) return;  // uniform over the CTA
+            odd = __syncthreads_or(!(none == 0.f));
+            if (odd) amax = 0.f;
         }
     }
-    each([&](int r, const Unit<VEC, INTER>& un, const float (&p)[VEC], const float (&q)[VEC]) {
-        int8_t* dst = codes + (long long)(r0 + r) * d;
-        store_codes<VEC>(dst + un.f0, p, inv, odd);
-        if (un.two) store_codes<VEC>(dst + un.f1, q, inv, odd);
-    });
     __syncthreads();  // everyone has read the old scale and `red`
     if (tid == 0) *scales = now;
 }
@@ -503,9 +507,12 @@ __device__ __forceinline__ void page_run(const AppendArgs& a, int i, const Token
 // Blocks [0, q_blocks): q heads of the tokens, one warp per share. The rest:
 // block x serves the page runs that start in tokens [chunk*x', chunk*(x'+1))
 // for one kv-head. Without Q (no queries, or the bulk form takes them) the code
-// for them does not hold registers, and three CTAs fit an SM instead of one.
+// for them is not there. Three CTAs per SM even at the price of some spills in
+// the queries' part: with one, a decode step of 64 tokens ran in two waves (10.0
+// us, with three 5.8). 16000 tokens into pages of 32 rows, 4 kv-heads: 23 us, and
+// 33 us for the queries.
 template <typename T, int VEC, bool INTER, bool Q>
-__global__ void __launch_bounds__(2 * kRunThreads, Q ? 1 : 3)
+__global__ void __launch_bounds__(2 * kRunThreads, 3)
 paged_append_q8_kernel(const AppendArgs a, int shares, int q_blocks, int chunk) {
     if (Q && (int)blockIdx.x < q_blocks) {
         const long long w = (long long)blockIdx.x * (2 * kRunThreads / 32) + threadIdx.x / 32;
