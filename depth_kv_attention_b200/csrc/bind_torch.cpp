@@ -155,6 +155,8 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int dev = k->get_device();
         const long long sq = q ? token_stride(where, *q, dev) : 0, sk = token_stride(where, *k, dev), sv = token_stride(where, *v, dev);
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+        const c10::cuda::CUDAStream stream = stream_of(a[16], dev, where);
+        const c10::cuda::CUDAStreamGuard on(stream);  // what is made here comes from the pool of the stream that writes it
         Tensor made;
         if (q && !qo) {
             made = at::empty({c.N, c.Hq, c.d}, q->options());
@@ -162,7 +164,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         moda_status st = MODA_OK;
         if (c.N > 0) {
-            void* s = stream_of(a[16], dev, where).stream();
+            void* s = stream.stream();
             const int rl = rope ? size32(rope->size(0), where) : 0, rot = rope ? size32(rope->size(1), where) : 0;
             const int Ld = kd ? size32(kd->size(1), where) : 0;
             auto i32 = [](const Tensor* t) { return static_cast<const int32_t*>(t->data_ptr()); };
@@ -212,6 +214,8 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
             bad(where, "fp32 lse [N,Hq] expected");
         const int dev = q->get_device();
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+        const c10::cuda::CUDAStream stream = stream_of(a[17], dev, where);
+        const c10::cuda::CUDAStreamGuard on(stream);  // what is made here comes from the pool of the stream that writes it
         Tensor made_out, made_lse, made_ws;
         if (!out) {
             made_out = at::empty(q->sizes(), q->options());
@@ -223,10 +227,8 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         moda_status st = MODA_OK;
         if (c.N > 0) {
-            const c10::cuda::CUDAStream stream = stream_of(a[17], dev, where);
             const size_t need = moda_fwd_paged_workspace_bytes(c.N, c.B, max_q, c.Hq, c.Hkv, c.d, c.pages, c.page, c.dt, q8);
             if (!ws && need) {
-                const c10::cuda::CUDAStreamGuard on(stream);  // from the pool of the stream it is used on
                 made_ws = at::empty({(int64_t)need}, q->options().dtype(at::kByte));
                 ws = &made_ws;
             }

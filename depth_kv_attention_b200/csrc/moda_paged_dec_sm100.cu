@@ -988,9 +988,9 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
     // The longest unit that the block table allows, in stages. Up to two stay
     // whole and save the join (one sequence of 16 tokens, G = 4: 8.6 us against
     // 9.4). Longer ones are cut to use the idle CTAs (one of 256 tokens: 9.8
-    // against 12.0; 64 rows of one kv-head 12.6 against 18.6), up to six stages
-    // only when there are units for a share of the CTAs anyway (64 sequences of
-    // 128, four tokens each: 33.1 cut, 23.8 whole).
+    // against 12.0), but for those of up to six stages when there are units for
+    // a share of the CTAs anyway (64 sequences of 128 tokens, four of them new,
+    // G = 4: 33.1 cut, 23.8 whole).
     const long long keys = (long long)c.max_blocks * c.page_size;
     const long long toks = std::min((C::MR + a.G - 2) / a.G + 1, a.max_q);
     const long long stages = (keys + C::KEYS - 1) / C::KEYS + (toks * p.DSL + C::DS - 1) / C::DS;

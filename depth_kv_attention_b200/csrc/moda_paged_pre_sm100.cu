@@ -21,6 +21,17 @@
 //  * Value tiles in which some row is masked pass through two conditioning
 //    warps, which clear their non-finite elements (a masked P is 0, and 0 * NaN
 //    is not); rows that do see one get it added back when the piece ends.
+//  * Code is kept small where a piece begins and ends: with short sequences the
+//    roles of 12 warps together miss the instruction cache all the time, and
+//    each piece of unrolled code cost more than it saved. For the same reason
+//    nothing spills: shared memory leaves the L1 cache almost no room.
+//
+// What bounds it: the products, while a unit is long (1024 tokens over 16K,
+// G = 8: 423 us, 65 % of the cuBLAS rate; a tile's softmax, 1 us an item, and
+// its own products alternate, so the two tiles together fill about 70 %). A
+// piece costs about 6 us besides: queries, first products, the last tile's
+// values and the epilogue follow each other (216-token sequences: 184 us for 42
+// us of products; one 2048-token prompt 98 for 21).
 //  * Every mbarrier wait is bounded, as in the dense forward.
 #include <cuda_bf16.h>
 
@@ -72,7 +83,8 @@ struct PreParams {
 
 // Warpgroups 0, 1: softmax of tiles 0, 1. Warps 8, 9: producer, MMA; 10, 11
 // condition. Registers at launch and after reallocation:
-// 384 x 168 = 256 x 216 + 128 x 72.
+// 384 x 168 = 256 x 200 + 128 x 104. (With 216 and 72 the control warps spilled:
+// 1024 tokens over 16K 473 us, with these 455.)
 constexpr int kThreads = 384;
 constexpr int kCondFirst = 10;
 constexpr int kCond = 64;        // conditioning threads
@@ -579,110 +591,112 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------ MMA warp -
-        {
-            const uint32_t lead = lane == 0;
-            constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, kItemKeys, 0, 0);
-            constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HALVES * 64, 0, 1);
-            const uint32_t sQa = ptx::smem_u32(sQ), sRa = ptx::smem_u32(sRing);
-            const uint64_t q0 = ptx::umma_desc_sw128(sQa, 16, 1024);
-            const uint64_t k0 = ptx::umma_desc_sw128(sRa, 16, 1024);
-            const uint64_t v0 = ptx::umma_desc_sw128(sRa, kHalfBytes, 1024);
-            constexpr uint64_t kSlotUnits = kTileBytes >> 4;
-            auto wait_one = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = ptx::mbar_wait(bar, parity, wait_limit, abort_flag);
-                if (got) ptx::tc_fence_after();
-                else flag_timeout(p, bars);
-                return got;
-            };
-            auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-                const bool got = __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, wait_limit, abort_flag));
-                if (got) ptx::tc_fence_after();
-                else if (lead) flag_timeout(p, bars);
-                return got;
-            };
-            auto issue_s_one = [&](int i, int st) {
-                const uint64_t kd_ = k0 + (uint64_t)st * kSlotUnits, qd_ = q0 + (uint64_t)i * kSlotUnits;
+        // -------------------------------------------------------- MMA warp
+        // One lane issues. The loop over plain items is that lane's alone; at a
+        // piece's ends, where instruction fetch is what costs, the whole warp
+        // walks and one lane's predicate issues: the code is smaller so.
+        const uint32_t lead = lane == 0;
+        constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, kItemKeys, 0, 0);
+        constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, HALVES * 64, 0, 1);
+        const uint32_t sQa = ptx::smem_u32(sQ), sRa = ptx::smem_u32(sRing);
+        const uint64_t q0 = ptx::umma_desc_sw128(sQa, 16, 1024);
+        const uint64_t k0 = ptx::umma_desc_sw128(sRa, 16, 1024);
+        const uint64_t v0 = ptx::umma_desc_sw128(sRa, kHalfBytes, 1024);
+        constexpr uint64_t kSlotUnits = kTileBytes >> 4;
+        auto wait_one = [&](uint64_t* bar, uint32_t parity) {
+            const bool got = ptx::mbar_wait(bar, parity, wait_limit, abort_flag);
+            if (got) ptx::tc_fence_after();
+            else flag_timeout(p, bars);
+            return got;
+        };
+        auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+            const bool got = __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, wait_limit, abort_flag));
+            if (got) ptx::tc_fence_after();
+            else if (lead) flag_timeout(p, bars);
+            return got;
+        };
+        auto issue_s_one = [&](int i, int st) {
+            const uint64_t kd_ = k0 + (uint64_t)st * kSlotUnits, qd_ = q0 + (uint64_t)i * kSlotUnits;
 #pragma unroll
+            for (int k = 0; k < 4 * HALVES; ++k) {
+                const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
+                ptx::mma_ss(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0);
+            }
+            ptx::mma_commit(&bars->s_full[i]);
+        };
+        auto issue_pv_one = [&](int i, uint64_t vd, bool add) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                ptx::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, vd + (uint64_t)(k * 128), idesc_pv,
+                            (add || k > 0) ? 1u : 0u);
+        };
+        uint32_t pp = 0;                 // p_full phases, a bit per tile
+        int st = 0;
+        uint32_t ph = 0;
+        auto advance = [&]() {
+            if (++st == kStages) {
+                st = 0;
+                ph ^= 1;
+            }
+        };
+        bool ok = true;
+        bool more = true;
+        for (int piece = 0; more && ok; ++piece) {
+            const Piece* w = take_piece(piece);
+            if (!__all_sync(0xffffffffu, w != nullptr)) {
+                if (lead) flag_timeout(p, bars);
+                break;
+            }
+            const Unit u = w->u;
+            const int first = w->first, end = w->end;
+            more = w->left > end - first;
+            __syncwarp();
+            if (lead) ptx::mbar_arrive(&bars->piece_empty[piece % kPieces]);
+            // the last item of each tile in the piece (first - 1: none)
+            int last0 = end - 1, last1 = u.ntok > n ? end - 1 : first - 1;
+            while (last0 >= first && !u.part(0, last0)) --last0;
+            while (last1 >= first && !u.part(1, last1)) --last1;
+            // Rolled, for the items at a piece's ends: unrolled, a batch of 216-token
+            // sequences took 230 us instead of 204
+            auto issue_tail = [&](int i, int x, int slot) {
+                const uint64_t kd_ = k0 + (uint64_t)slot * kSlotUnits, qd_ = q0 + (uint64_t)i * kSlotUnits;
+#pragma unroll 1
                 for (int k = 0; k < 4 * HALVES; ++k) {
                     const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
-                    ptx::mma_ss(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0);
+                    ptx::mma_ss_lead(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0, lead);
                 }
-                ptx::mma_commit(&bars->s_full[i]);
+                ptx::mma_commit_lead(&bars->s_full[i], lead);
+                // after its last product the tile's queries may go
+                if (x == (i ? last1 : last0)) ptx::mma_commit_lead(&bars->q_empty[i], lead);
             };
-            auto issue_pv_one = [&](int i, uint64_t vd, bool add) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    ptx::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, vd + (uint64_t)(k * 128), idesc_pv,
-                                (add || k > 0) ? 1u : 0u);
+            // o_final may run at most one piece ahead of either tile's warps,
+            // also of a tile that takes no part in these pieces
+            auto finish = [&](int i) {
+                if (piece > 0 && !wait_all(&bars->o_empty[i], (piece - 1) & 1)) return false;
+                ptx::mma_commit_lead(&bars->o_final[i], lead);
+                return true;
             };
-            uint32_t pp = 0;                 // p_full phases, a bit per tile
-            int st = 0;
-            uint32_t ph = 0;
-            auto advance = [&]() {
-                if (++st == kStages) {
-                    st = 0;
-                    ph ^= 1;
-                }
-            };
-            bool ok = true;
-            bool more = true;
-            for (int piece = 0; more && ok; ++piece) {
-                const Piece* w = take_piece(piece);
-                if (!__all_sync(0xffffffffu, w != nullptr)) {
-                    if (lead) flag_timeout(p, bars);
-                    break;
-                }
-                const Unit u = w->u;
-                const int first = w->first, end = w->end;
-                more = w->left > end - first;
-                __syncwarp();
-                if (lead) ptx::mbar_arrive(&bars->piece_empty[piece % kPieces]);
-                // the last item of each tile in the piece (first - 1: none)
-                int last0 = end - 1, last1 = u.ntok > n ? end - 1 : first - 1;
-                while (last0 >= first && !u.part(0, last0)) --last0;
-                while (last1 >= first && !u.part(1, last1)) --last1;
-                // Rolled forms for the items at a piece's ends (the instruction
-                // cache again); `who` bits: the tiles that take part
-                auto issue_tail = [&](int i, int x, int slot) {
-                    const uint64_t kd_ = k0 + (uint64_t)slot * kSlotUnits, qd_ = q0 + (uint64_t)i * kSlotUnits;
+            auto who = [&](int x) { return (u.part(0, x) ? 1u : 0u) | (u.part(1, x) ? 2u : 0u); };
+            uint32_t cur = who(first), started = 0;
+            ok = wait_all(&bars->full[st], ph);
 #pragma unroll 1
-                    for (int k = 0; k < 4 * HALVES; ++k) {
-                        const uint64_t off = (uint64_t)((k >> 2) * (kHalfBytes >> 4) + (k & 3) * 2);
-                        ptx::mma_ss_lead(tmem + i * 128, qd_ + off, kd_ + off, idesc_qk, k > 0, lead);
-                    }
-                    ptx::mma_commit_lead(&bars->s_full[i], lead);
-                    // after its last product the tile's queries may go
-                    if (x == (i ? last1 : last0)) ptx::mma_commit_lead(&bars->q_empty[i], lead);
-                };
-                // o_final may run at most one piece ahead of either tile's warps,
-                // also of a tile that takes no part in these pieces
-                auto finish = [&](int i) {
-                    if (piece > 0 && !wait_all(&bars->o_empty[i], (piece - 1) & 1)) return false;
-                    ptx::mma_commit_lead(&bars->o_final[i], lead);
-                    return true;
-                };
-                auto who = [&](int x) { return (u.part(0, x) ? 1u : 0u) | (u.part(1, x) ? 2u : 0u); };
-                uint32_t cur = who(first), started = 0;
-                ok = wait_all(&bars->full[st], ph);
-#pragma unroll 1
-                for (int i = 0; i < 2 && ok; ++i) {
-                    ok = wait_all(&bars->q_full[i], piece & 1);
-                    if (!ok) break;
-                    if ((cur >> i) & 1) issue_tail(i, first, st);
-                    if ((i ? last1 : last0) < first) {
-                        ptx::mma_commit_lead(&bars->q_empty[i], lead);
-                        ok = finish(i);
-                    }
-                }
+            for (int i = 0; i < 2 && ok; ++i) {
+                ok = wait_all(&bars->q_full[i], piece & 1);
                 if (!ok) break;
-                ptx::mma_commit_lead(&bars->empty[st], lead);
-                advance();
-                // Items that both tiles take part in, as in the next one, and that
-                // are nobody's last: the loop that has to keep the tensor core fed
-                const int plain = min(end - 2, min(u.nkv0, u.nkv1) - 2);
-                int x = first;
-                if (lead) {
+                if ((cur >> i) & 1) issue_tail(i, first, st);
+                if ((i ? last1 : last0) < first) {
+                    ptx::mma_commit_lead(&bars->q_empty[i], lead);
+                    ok = finish(i);
+                }
+            }
+            if (!ok) break;
+            ptx::mma_commit_lead(&bars->empty[st], lead);
+            advance();
+            // Items that both tiles take part in, as in the next one, and that
+            // are nobody's last: the loop that has to keep the tensor core fed
+            const int plain = min(end - 2, min(u.nkv0, u.nkv1) - 2);
+            int x = first;
+            if (lead) {
                 for (; x < plain; ++x) {
                     const int st_v = st;
                     if (!(ok = wait_one(&bars->full[st], ph))) break;
@@ -702,70 +716,69 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                     pp ^= 3;
                     started = 3;
                 }
-                }
-                __syncwarp();
-                x = __shfl_sync(0xffffffffu, x, 0);
-                st = __shfl_sync(0xffffffffu, st, 0);
-                ph = __shfl_sync(0xffffffffu, ph, 0);
-                pp = __shfl_sync(0xffffffffu, pp, 0);
-                started = __shfl_sync(0xffffffffu, started, 0);
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-                if (x > first) cur = 3;
-                for (; x < end && ok; ++x) {
-                    const int st_v = st;
-                    ok = wait_all(&bars->full[st], ph);
-                    if (!ok) break;
-                    advance();
-                    const bool next = x + 1 < end;
-                    const uint64_t vd = v0 + (uint64_t)st_v * kSlotUnits;
-                    const uint32_t nxt = next ? who(x + 1) : 0u;
-                    bool k_ready = false;
-                    // round 0: a tile that sits this item out can go ahead with the
-                    // next; then tile 0's and tile 1's P V and next S
-#pragma unroll 1
-                    for (int step = 0; step < 4 && ok; ++step) {
-                        const int i = step & 1;
-                        const bool in = (cur >> i) & 1;
-                        if (step < 2 ? in : !in) continue;
-                        if (in) {
-                            // (P also says that this tile's warps have read the O of the
-                            // piece before, which the piece's first P V overwrites)
-                            if (!wait_all(&bars->p_full[i], (pp >> i) & 1)) {
-                                ok = false;
-                                break;
-                            }
-                            pp ^= 1u << i;
-#pragma unroll 1
-                            for (int k = 0; k < 8; ++k)
-                                ptx::mma_ts_lead(tmem + 256 + i * 128, tmem + i * 128 + k * 8, vd + (uint64_t)(k * 128), idesc_pv,
-                                            ((started >> i) & 1) | (k > 0 ? 1u : 0u), lead);
-                            started |= 1u << i;
-                            if (x == (i ? last1 : last0) && !finish(i)) {
-                                ok = false;
-                                break;
-                            }
-                        }
-                        if ((nxt >> i) & 1) {
-                            if (!k_ready && !wait_all(&bars->full[st], ph)) {
-                                ok = false;
-                                break;
-                            }
-                            k_ready = true;
-                            issue_tail(i, x + 1, st);
-                        }
-                    }
-                    if (!ok) break;
-                    ptx::mma_commit_lead(&bars->empty[st_v], lead);
-                    if (next) {
-                        ptx::mma_commit_lead(&bars->empty[st], lead);
-                        advance();
-                    }
-                    cur = nxt;
-                }
             }
-            ptx::mma_commit_lead(&bars->drain, lead);
-            ptx::mbar_wait(&bars->drain, 0, kNoPollLimit, nullptr);
+            __syncwarp();
+            x = __shfl_sync(0xffffffffu, x, 0);
+            st = __shfl_sync(0xffffffffu, st, 0);
+            ph = __shfl_sync(0xffffffffu, ph, 0);
+            pp = __shfl_sync(0xffffffffu, pp, 0);
+            started = __shfl_sync(0xffffffffu, started, 0);
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+            if (x > first) cur = 3;
+            for (; x < end && ok; ++x) {
+                const int st_v = st;
+                ok = wait_all(&bars->full[st], ph);
+                if (!ok) break;
+                advance();
+                const bool next = x + 1 < end;
+                const uint64_t vd = v0 + (uint64_t)st_v * kSlotUnits;
+                const uint32_t nxt = next ? who(x + 1) : 0u;
+                bool k_ready = false;
+                // round 0: a tile that sits this item out can go ahead with the
+                // next; then tile 0's and tile 1's P V and next S
+#pragma unroll 1
+                for (int step = 0; step < 4 && ok; ++step) {
+                    const int i = step & 1;
+                    const bool in = (cur >> i) & 1;
+                    if (step < 2 ? in : !in) continue;
+                    if (in) {
+                        // (P also says that this tile's warps have read the O of the
+                        // piece before, which the piece's first P V overwrites)
+                        if (!wait_all(&bars->p_full[i], (pp >> i) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        pp ^= 1u << i;
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k)
+                            ptx::mma_ts_lead(tmem + 256 + i * 128, tmem + i * 128 + k * 8, vd + (uint64_t)(k * 128), idesc_pv,
+                                        ((started >> i) & 1) | (k > 0 ? 1u : 0u), lead);
+                        started |= 1u << i;
+                        if (x == (i ? last1 : last0) && !finish(i)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if ((nxt >> i) & 1) {
+                        if (!k_ready && !wait_all(&bars->full[st], ph)) {
+                            ok = false;
+                            break;
+                        }
+                        k_ready = true;
+                        issue_tail(i, x + 1, st);
+                    }
+                }
+                if (!ok) break;
+                ptx::mma_commit_lead(&bars->empty[st_v], lead);
+                if (next) {
+                    ptx::mma_commit_lead(&bars->empty[st], lead);
+                    advance();
+                }
+                cur = nxt;
+            }
         }
+        ptx::mma_commit_lead(&bars->drain, lead);
+        ptx::mbar_wait(&bars->drain, 0, kNoPollLimit, nullptr);
         __syncwarp();
     } else if (warp >= kCondFirst) {
         // ---------------------------------------------------- conditioning
@@ -952,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
     ptx::tc_fence_before();
     __syncthreads();
     // the join may be scheduled once every CTA is about here; earlier its
-    // waiting blocks would take issue slots from this kernel (QQ)
+    // waiting blocks would take issue slots from this kernel
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) {
         ptx::tc_fence_after();

@@ -5,8 +5,10 @@
 // One softmax over the token's visible sequence keys and its own depth keys
 // ("动态混合深度注意力机制MoDA技术解析", mhpn.cn, §1.2 formula; §2.2 online softmax
 // state and the dual mask). One CTA per (token, query head); eight lanes share
-// a key (four consecutive features of every 32 each), so a warp works on four
-// keys at once, each lane group with its own running (m, l, o). The states are
+// a key (four consecutive features of every 32 each), each lane group has two
+// keys in flight and its own running (m, l, o), so a warp works on eight keys
+// at once. Small calls are a chain of loads (48 tokens in four sequences: 6 us);
+// larger ones are bound by instructions, about 50 per key and lane. The states are
 // joined by shuffles within a warp and through shared memory across warps.
 // Only visible keys are touched, so nothing masked can reach a sum.
 #include <cuda_bf16.h>
@@ -188,7 +190,7 @@ cudaError_t launch_paged_fwd_simt(const PagedFwdArgs& a, cudaStream_t s) {
     const PagedCache& c = a.c;
     const long long grid = (long long)c.N * a.Hq;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    // a warp takes four keys at a time: about eight rounds before more warps help
+    // a warp takes eight keys at a time: up to four rounds before more warps help
     const long long keys = (long long)c.max_blocks * c.page_size;
     int warps = 2;
     while (warps < kMaxWarps && keys > (long long)warps * 32) warps *= 2;

@@ -441,14 +441,14 @@ moda_status moda_paged_append_q8(const void* q, const void* k, const void* v,
  *   workspace  in  device scratch of >= moda_fwd_paged_workspace_bytes(...),
  *                  16-byte aligned, contents on entry ignored (may be NULL
  *                  when that is 0). Calls that share it must not overlap. For
- *                  chunks over 8-bit pages (max_q * G of 65 and more; q8 != 0 in
- *                  the size's call) it also holds the pages in use
- *                  as bf16, in two pools of num_pages pages; one workspace
- *                  serves all layers.
+ *                  chunks over 8-bit pages (max_q * Hq / Hkv of 33 and more;
+ *                  q8 != 0 in the size's call) it also holds the pages in
+ *                  use as bf16, in two pools of num_pages pages; one
+ *                  workspace serves all layers.
  * The attention does not append: call moda_paged_append first, with the same
  * cu_q, ctx_lens and block_table. moda_fwd_paged_q8 reads 8-bit pages; depth
- * rows stay in `dtype`. bf16 with d % 8 == 0 and page_size % 16 == 0 runs on
- * the tensor cores, everything else on the SIMT kernels (MODA_IMPL_TC2 is not
+ * rows stay in `dtype`. bf16 with d % 8 == 0 (8-bit pages: d % 16 == 0) and
+ * page_size % 16 == 0 runs on the tensor cores, everything else on the SIMT kernels (MODA_IMPL_TC2 is not
  * offered: MODA_ERR_UNSUPPORTED). Errors otherwise as moda_fwd_ex.
  */
 size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d,

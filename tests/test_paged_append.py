@@ -256,3 +256,26 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(bits(a), b) for a, b in zip([out] + pages, w))
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
+def test_pages_past_32_bits(q8):
+    """The same rows arrive in pages whose elements lie 2^31 from the pool's start."""
+    c = Paged("far", ((300, 200), (77, 1)), Hq=8, Hkv=1, rot=64, P=64)
+    x = make(c, dev="cuda")
+    n = x["k_pages"].shape[0]
+    first = 2 ** 31 // (c.Hkv * c.P * c.d) - 3
+    dt = torch.int8 if q8 else torch.bfloat16
+    pools = []
+    for pages in (n, first + n):
+        kv = [torch.empty((pages, c.Hkv, c.P, c.d), dtype=dt, device="cuda") for _ in range(2)]
+        sc = [torch.empty((pages, c.Hkv), device="cuda") for _ in range(2)] if q8 else []
+        for t in kv + sc:
+            t[-n:] = 0
+        table = torch.where(x["table"] < 0, x["table"], x["table"] + (pages - n))
+        f = moda.moda_paged_append_q8 if q8 else moda.moda_paged_append
+        f(x["q"], x["k"], x["v"], *kv, *sc, table, x["cu_q"], x["ctx"], rope=x["rope"])
+        pools.append(kv + sc)
+    torch.cuda.synchronize()
+    for near, far in zip(*pools):
+        assert near.any() and torch.equal(near, far[first:])

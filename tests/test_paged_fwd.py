@@ -46,6 +46,8 @@ CASES = [
     Paged("chunk_many", tuple((20 + 7 * b, (5 * b) % 17) for b in range(40)), Hq=12, Hkv=2, Ld=3, cap=3),
     Paged("chunk_short_ctx", ((5, 70), (3, 40), (0, 30)), Hq=4, Hkv=1),
     Paged("chunk_short_depth", ((5, 70), (3, 40), (0, 30)), Hq=4, Hkv=1, Ld=4, cap=4),
+    Paged("chunk_long_g33", ((2100, 11), (700, 3)), Hq=33, Hkv=1, Ld=20, cap=20, d=64, P=48),
+    Paged("rows33", ((900, 33), (1500, 9)), Hq=4, Hkv=4, Ld=4, cap=4, d=96),
     Paged("deep", steps(40), Hq=4, Hkv=1, Ld=130, cap=140),
     Paged("short_ctx", ((2, 5), (0, 1), (3, 3)), Hq=8, Hkv=2),
     Paged("short_ctx_depth", ((2, 5), (0, 1), (3, 3)), Hq=8, Hkv=2, Ld=3, cap=3),
@@ -94,6 +96,17 @@ def test_parity(c, q8, impl):
     check_rows(out, lse, want(x, c), c.dtype, keys_of(c), c.d, c.name)
     n = c.N - c.spare_rows
     assert torch.all(out[n:] == 9) and torch.all(lse[n:] == 9)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
+def test_long_chunks(q8):
+    """Many key tiles per part; parts that end inside a unit and begin in the next."""
+    c = Paged("chunk_long", ((3000, 300), (2500, 260)), Hq=16, Hkv=2, Ld=5, cap=5, P=64, d=96)
+    x = make(c, q8=q8)
+    got = run(cuda(x), c, q8)
+    torch.cuda.synchronize()
+    assert moda.moda_device_status() == 0
+    check_rows(*got, want(x, c), c.dtype, keys_of(c), c.d)
 
 
 @pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
@@ -308,3 +321,59 @@ def test_layers_of_steps(q8):
             check_rows(out, lse, w, "bf16", max(ctx) + layer, d)
             turned = oracle.rotate(k[0].double().cpu().numpy(), rope[ctx[0] - new[0]].double().cpu().numpy(), False)
             assert abs(kd[0, layer].double().cpu().numpy() - turned).max() <= 2.0 ** -8 * abs(turned).max() + 1e-5
+
+
+@pytest.mark.parametrize("new", [1, 40], ids=["step", "chunk"])
+@pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
+def test_sequences_with_a_common_beginning(q8, new):
+    """Pages that stand in several tables, and twice in one."""
+    c = Paged("prefix", ((200, new), (170, new), (96, new)), Hq=8, Hkv=2, Ld=2, cap=2, P=16)
+    x = make(c, q8=q8)
+    x["table"][1, :6] = x["table"][0, :6]
+    x["table"][2, :3] = x["table"][0, 3:6]
+    x["table"][2, 3:6] = x["table"][0, 3:6]
+    got = run(cuda(x), c, q8)
+    torch.cuda.synchronize()
+    check_rows(*got, want(x, c), c.dtype, keys_of(c), c.d)
+
+
+@pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
+def test_two_streams_at_once(q8):
+    """Steps and chunks side by side on two streams, each with what it allocates."""
+    calls = []
+    for seqs in (((3000, 1), (1500, 2), (10, 1)), ((1200, 300), (90, 64))):
+        c = Paged("side", seqs, Hq=32, Hkv=4, Ld=6, cap=6)
+        calls.append((c, cuda(make(c, q8=q8))))
+    alone = [run(x, c, q8) for c, x in calls]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, x) in enumerate(calls):
+            got[i].append(run(x, c, q8, stream=side[i]))
+    torch.cuda.synchronize()
+    assert moda.moda_device_status() == 0
+    for a, g in zip(alone, got):
+        for o, l in g:
+            assert torch.equal(o, a[0]) and torch.equal(l, a[1])
+
+
+@pytest.mark.parametrize("impl", ["auto", "simt"])
+@pytest.mark.parametrize("q8", [False, True], ids=["kv16", "kv8"])
+@pytest.mark.parametrize("new", [1, 40], ids=["step", "chunk"])
+def test_pages_past_32_bits(new, q8, impl):
+    """Pages whose elements lie 2^31 and more from the pool's start."""
+    c = Paged("far", ((300, new), (77, new)), Hq=8, Hkv=1, Ld=2, cap=2, P=64)
+    x = make(c, q8=q8)
+    n = x["k_pages"].shape[0]
+    first = 2 ** 31 // (c.Hkv * c.P * c.d) - 3   # of n pages that lie across the mark
+    far = cuda(x)
+    for name in ("k_pages", "v_pages", "k_scale", "v_scale"):
+        if name in far:
+            pool = torch.empty((first + n, *x[name].shape[1:]), dtype=x[name].dtype, device="cuda")
+            pool[first:] = far[name]
+            far[name] = pool
+    far["table"] = torch.where(far["table"] < 0, far["table"], far["table"] + first)
+    got = run(far, c, q8, impl)
+    torch.cuda.synchronize()
+    check_rows(*got, want(x, c), c.dtype, keys_of(c), c.d)
