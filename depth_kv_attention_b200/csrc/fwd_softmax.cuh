@@ -34,11 +34,13 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 #endif
 constexpr int kPolyFrom = MODA_POLY_FROM;
 
-// mask(s): sets the columns of s this row does not see to -inf.
+// seq_item: a causal sequence tile whose first key is kbase (row token t);
+// otherwise a depth chunk in which this row's own depth columns start at
+// dep_lo (negative or >= 128 when they begin before or after the chunk).
 // it: items this row has taken part in before (0 = O holds nothing yet).
-template <typename Mask>
-__device__ __forceinline__ void softmax_columns(uint32_t tS, uint32_t tO, Mask&& mask, float sl2, int it, float& m,
-                                                float& l) {
+__device__ __forceinline__ void softmax_item(uint32_t tS, uint32_t tO, bool seq_item, int kbase, int t,
+                                             int dep_lo, int Ld, bool has_sel, unsigned long long sel,
+                                             float sl2, int it, float& m, float& l) {
     float s[128];
     {
         uint32_t su[128];
@@ -48,7 +50,20 @@ __device__ __forceinline__ void softmax_columns(uint32_t tS, uint32_t tO, Mask&&
 #pragma unroll
         for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(su[c]);
     }
-    mask(s);
+    if (seq_item) {
+        if (kbase + 127 > t) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+                if (kbase + c > t) s[c] = -INFINITY;
+        }
+    } else {
+        // same-token mask: this row's depth columns (selected slots only)
+        uint32_t vis[4];
+        depth_col_mask(dep_lo, Ld, has_sel, sel, vis);
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+            if (!((vis[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
+    }
     float mx;
     {
         float mp[8];
@@ -111,33 +126,6 @@ __device__ __forceinline__ void softmax_columns(uint32_t tS, uint32_t tO, Mask&&
         const float2 a = ptx::add2(a01, a23);
         l += a.x + a.y;
     }
-}
-
-// seq_item: a causal sequence tile whose first key is kbase (row token t);
-// otherwise a depth chunk in which this row's own depth columns start at
-// dep_lo (negative or >= 128 when they begin before or after the chunk).
-__device__ __forceinline__ void softmax_item(uint32_t tS, uint32_t tO, bool seq_item, int kbase, int t,
-                                             int dep_lo, int Ld, bool has_sel, unsigned long long sel,
-                                             float sl2, int it, float& m, float& l) {
-    softmax_columns(
-        tS, tO,
-        [&](float (&s)[128]) {
-            if (seq_item) {
-                if (kbase + 127 > t) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (kbase + c > t) s[c] = -INFINITY;
-                }
-            } else {
-                // same-token mask: this row's depth columns (selected slots only)
-                uint32_t vis[4];
-                depth_col_mask(dep_lo, Ld, has_sel, sel, vis);
-#pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if (!((vis[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
-            }
-        },
-        sl2, it, m, l);
 }
 
 }  // namespace moda

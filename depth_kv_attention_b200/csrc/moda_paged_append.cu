@@ -31,7 +31,7 @@
 #include <algorithm>
 
 #include "paged_common.cuh"
-#include "sm100_ptx.cuh"
+#include "paged_ptx.cuh"
 #include "smem_limit.h"
 
 namespace moda {

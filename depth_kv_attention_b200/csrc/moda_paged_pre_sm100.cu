@@ -42,8 +42,8 @@
 #include "depth_mask.cuh"
 #include "fwd_softmax.cuh"
 #include "paged_join.cuh"
+#include "paged_ptx.cuh"
 #include "paged_units.cuh"
-#include "sm100_ptx.cuh"
 #include "tmap_host.h"
 
 namespace moda {
@@ -249,7 +249,7 @@ struct Piece {
 
 static_assert(sizeof(PreBars) + kPieces * sizeof(Piece) <= kCtl && sizeof(PreBars) % 8 == 0, "control block");
 
-// softmax_columns for an item of which the row sees columns [lo, hi) less those
+// softmax_item for an item of which the row sees columns [lo, hi) less those
 // in `holes` (bit k: columns 16 k ..). In chunks of 32 columns, read twice, in
 // rolled loops: items like this are a few per unit, and the unrolled code of
 // 128 masked columns (26 KB of it) pushed everything else out of the
@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_pre_kernel(const __grid_con
                     hi = lo + p.Ld;
                 }
                 if (__all_sync(0xffffffffu, seq && hi >= 128) && !holes)
-                    softmax_columns(tS, tO, [](float (&)[128]) {}, p.sl2, it, m, l);
+                    softmax_item(tS, tO, true, 0, 127, 0, 0, false, 0, p.sl2, it, m, l);  // nothing to mask
                 else
                     softmax_masked(tS, tO, lo, hi, holes, p.sl2, it, m, l);
                 __syncwarp();

@@ -113,14 +113,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_lead(uint64_t* bar, uint32
         "r"(bytes), "r"(leader)
         : "memory");
 }
-// Untiled bulk copy into this CTA's shared memory: both addresses 16-byte
-// aligned, a multiple of 16 bytes; completion counted on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
 // 4-D tiled load into shared memory, completion counted on `bar` (bytes).
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0,
                                             int c1, int c2, int c3) {
@@ -478,13 +470,6 @@ __device__ __forceinline__ bool bar_and(uint32_t id, uint32_t n, bool v) {
 }
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t n) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-
-// One 32-byte store (a whole sector); the address is 32-byte aligned.
-__device__ __forceinline__ void st_global_32b(void* dst, const uint32_t* v) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
