@@ -998,15 +998,17 @@ cudaError_t launch_halves(const PagedFwdArgs& a, char* ws, cudaStream_t s) {
         if (!make_tmap_bf16_4d(&p.tm_k, a.k_pages, dims, st, box) || !make_tmap_bf16_4d(&p.tm_v, a.v_pages, dims, st, box))
             return cudaErrorInvalidValue;
     }
-    if (a.Ld > 0) {
-        const cuuint64_t dims[4] = {d, Hkv, (cuuint64_t)a.Ld, (cuuint64_t)c.N};
-        const cuuint64_t st[3] = {d * 2, Hkv * d * 2, (cuuint64_t)a.Ld_cap * Hkv * d * 2};
+    {
+        // Without depth rows a unit that sees no key still has one item, all of
+        // it masked: boxes of the same size, anywhere in the pages.
+        const bool any = a.Ld > 0;
+        const cuuint64_t dims[4] = {d, Hkv, any ? (cuuint64_t)a.Ld : P, (cuuint64_t)(any ? c.N : c.num_pages)};
+        const cuuint64_t st[3] = {any ? d * 2 : P * d * 2, any ? Hkv * d * 2 : d * 2,
+                                  (cuuint64_t)(any ? a.Ld_cap : P) * Hkv * d * 2};
         const cuuint32_t box[4] = {64, 1, 16, 1};
-        if (!make_tmap_bf16_4d(&p.tm_kd, a.kd, dims, st, box) || !make_tmap_bf16_4d(&p.tm_vd, a.vd, dims, st, box))
+        if (!make_tmap_bf16_4d(&p.tm_kd, any ? a.kd : a.k_pages, dims, st, box) ||
+            !make_tmap_bf16_4d(&p.tm_vd, any ? a.vd : a.v_pages, dims, st, box))
             return cudaErrorInvalidValue;
-    } else {
-        p.tm_kd = p.tm_k;
-        p.tm_vd = p.tm_v;
     }
     p.c = c;
     p.v_pages = static_cast<const __nv_bfloat16*>(a.v_pages);

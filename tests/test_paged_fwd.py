@@ -47,6 +47,8 @@ CASES = [
     Paged("chunk_short_ctx", ((5, 70), (3, 40), (0, 30)), Hq=4, Hkv=1),
     Paged("chunk_short_depth", ((5, 70), (3, 40), (0, 30)), Hq=4, Hkv=1, Ld=4, cap=4),
     Paged("chunk_long_g33", ((2100, 11), (700, 3)), Hq=33, Hkv=1, Ld=20, cap=20, d=64, P=48),
+    Paged("chunk_sees_nothing", ((0, 30), (5, 70), (300, 20)), Hq=4, Hkv=1, P=128),
+    Paged("chunk_sees_nothing_g1", ((0, 50),), Hq=2, Hkv=2, P=64, d=64),
     Paged("rows33", ((900, 33), (1500, 9)), Hq=4, Hkv=4, Ld=4, cap=4, d=96),
     Paged("deep", steps(40), Hq=4, Hkv=1, Ld=130, cap=140),
     Paged("short_ctx", ((2, 5), (0, 1), (3, 3)), Hq=8, Hkv=2),
