@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cstring>
 
 #include "paged_common.cuh"
 #include "paged_ptx.cuh"
@@ -270,6 +271,8 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_bulk_kernel(const Ap
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, d = c.d;
     const int row_bytes = heads_per * d * (int)sizeof(T), rope_bytes = a.rope ? a.rot * 4 : 0;
     uint8_t* buf = smem + (size_t)warp * 2 * (row_bytes + rope_bytes);
+    // the keys and values of 8-bit pages, which need nothing of this, may start
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (lane == 0) {
         ptx::mbar_init(&bars[warp][0], 1);
         ptx::mbar_init(&bars[warp][1], 1);
@@ -552,6 +555,9 @@ paged_append_q8_kernel(const AppendArgs a, int shares, int q_blocks, int chunk) 
         run.taken = true;
         page_run<T, VEC, INTER>(a, (int)i0 + e, run, g, red);
     }
+    // Beside the bulk form's queries (see launch): what comes next in the stream
+    // has to find those done too, so one block outlasts them.
+    if (!Q && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // From this many bytes of q, k and v the bulk form is the faster one. Measured
@@ -606,8 +612,23 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
         const long long q_blocks = a.q && !bulk ? ((long long)c.N * shares + 7) / 8 : 0;
         const long long all = q_blocks + ((long long)c.N + chunk - 1) / chunk * c.Hkv;
         if (all > 0x7fffffffLL) return cudaErrorInvalidValue;
-        if (q_blocks) paged_append_q8_kernel<T, VEC, INTER, true><<<(unsigned)all, 2 * kRunThreads, 0, s>>>(a, shares, (int)q_blocks, chunk);
-        else paged_append_q8_kernel<T, VEC, INTER, false><<<(unsigned)all, 2 * kRunThreads, 0, s>>>(a, shares, 0, chunk);
+        if (q_blocks) {
+            paged_append_q8_kernel<T, VEC, INTER, true><<<(unsigned)all, 2 * kRunThreads, 0, s>>>(a, shares, (int)q_blocks, chunk);
+        } else {
+            // beside the queries' kernel, where that went ahead (16000 tokens: 56 us one
+            // after the other, 51 side by side; one of 4096 37 and 30)
+            cudaLaunchConfig_t cfg;
+            std::memset(&cfg, 0, sizeof(cfg));
+            cfg.gridDim = dim3((unsigned)all);
+            cfg.blockDim = dim3(2 * kRunThreads);
+            cfg.stream = s;
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = at;
+            cfg.numAttrs = bulk ? 1 : 0;
+            return cudaLaunchKernelEx(&cfg, paged_append_q8_kernel<T, VEC, INTER, false>, a, shares, 0, chunk);
+        }
     }
     return cudaGetLastError();
 }

@@ -279,3 +279,44 @@ def test_pages_past_32_bits(q8):
     torch.cuda.synchronize()
     for near, far in zip(*pools):
         assert near.any() and torch.equal(near, far[first:])
+
+
+def test_what_follows_finds_8bit_append_done():
+    """Many queries beside few keys: the kernel after the call, in a stream and
+    in a replayed graph, reads finished queries, codes and scales."""
+    c = Paged("after", ((4100, 4096),), Hq=64, Hkv=1, rot=128, P=64)
+    x = make(c, q8=True, dev="cuda")
+    pools = [x[n] for n in ("k_pages", "v_pages", "k_scale", "v_scale")]
+    src = [x[n].clone() for n in ("q", "k", "v")]
+    out = torch.empty_like(x["q"])
+
+    def call():
+        moda.moda_paged_append_q8(*src, *pools, x["table"], x["cu_q"], x["ctx"], rope=x["rope"], q_out=out)
+        return [t.clone() for t in (out, *pools)]
+
+    wanted = []
+    for f in (1, -2):
+        for n, t in zip(("q", "k", "v"), src):
+            t.copy_(x[n] * f)
+        call()
+        torch.cuda.synchronize()
+        wanted.append([t.clone() for t in (out, *pools)])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for rep in range(6):
+        f = rep % 2
+        for n, t in zip(("q", "k", "v"), src):
+            t.copy_(x[n] * (1, -2)[f])
+        out.zero_()
+        if rep < 4:
+            graph.replay()
+            seen = [t.clone() for t in got]
+        else:
+            seen = call()
+        torch.cuda.synchronize()
+        # (the page that holds earlier tokens keeps the larger scale of the two calls)
+        assert torch.equal(bits(seen[0]), bits(wanted[f][0]))
+        last = x["table"][0].long()[1:]
+        for a, b in zip(seen[1:], wanted[f][1:]):
+            assert torch.equal(bits(a[last]), bits(b[last]))
