@@ -32,11 +32,11 @@ struct alignas(sizeof(T) * 4) Four {
     T x[4];
 };
 
-// Features 32c + 4l .. +3 of a row, c = 0..3 (zero past d; d % 4 == 0).
-template <typename T>
-__device__ __forceinline__ void load16(const T* row, int d, int l, T (&x)[16]) {
+// Features 32c + 4l .. +3 of a row, c < F / 4 (zero past d; d % 4 == 0).
+template <int F, typename T>
+__device__ __forceinline__ void load_row(const T* row, int d, int l, T (&x)[F]) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < F / 4; ++c) {
         const int f = 32 * c + 4 * l;
         Four<T> v{};
         if (f < d) v = *reinterpret_cast<const Four<T>*>(row + f);
@@ -45,12 +45,14 @@ __device__ __forceinline__ void load16(const T* row, int d, int l, T (&x)[16]) {
     }
 }
 
+// F features a lane: 8 for d <= 64, else 16.
+template <int F>
 struct State {
-    float m, l, o[16];
+    float m, l, o[F];
     // Keys with logits s (log2 domain) and values v times sv; a logit of -inf
     // adds nothing (its values are zeros then).
     template <typename KV>
-    __device__ __forceinline__ void add(const float (&s)[kKeys], const KV (&v)[kKeys][16], const float (&sv)[kKeys]) {
+    __device__ __forceinline__ void add(const float (&s)[kKeys], const KV (&v)[kKeys][F], const float (&sv)[kKeys]) {
         float mn = m;
 #pragma unroll
         for (int u = 0; u < kKeys; ++u) mn = fmaxf(mn, s[u]);
@@ -58,13 +60,13 @@ struct State {
         const float corr = exp2f(m - ref);
         l *= corr;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] *= corr;
+        for (int e = 0; e < F; ++e) o[e] *= corr;
 #pragma unroll
         for (int u = 0; u < kKeys; ++u) {
             const float p = exp2f(s[u] - ref), pv = p * sv[u];
             l += p;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = fmaf(pv, pg_to_f(v[u][e]), o[e]);
+            for (int e = 0; e < F; ++e) o[e] = fmaf(pv, pg_to_f(v[u][e]), o[e]);
         }
         m = mn;
     }
@@ -75,12 +77,12 @@ struct State {
         const float c1 = exp2f(m - ref), c2 = exp2f(m2 - ref);
         l = l * c1 + l2 * c2;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = o[e] * c1 + __shfl_xor_sync(0xffffffffu, o[e], mask) * c2;
+        for (int e = 0; e < F; ++e) o[e] = o[e] * c1 + __shfl_xor_sync(0xffffffffu, o[e], mask) * c2;
         m = mn;
     }
 };
 
-template <typename T, typename KV>
+template <typename T, typename KV, int F>
 __global__ void __launch_bounds__(kMaxWarps * 32) paged_fwd_simt_kernel(const PagedFwdArgs a) {
     __shared__ float sm[kMaxWarps], sl[kMaxWarps], so[kMaxWarps][kDMax];
     const PagedCache& c = a.c;
@@ -90,31 +92,31 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_fwd_simt_kernel(const Pa
     const long long pos = (long long)__ldg(c.ctx_lens + b) - ((long long)__ldg(c.cu_q + b + 1) - i);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
     const int grp = warp * 4 + lane / 8, groups = warps * 4, l8 = lane % 8;
-    T q[16];
-    load16(static_cast<const T*>(a.q) + ((long long)i * a.Hq + h) * d, d, l8, q);
+    T q[F];
+    load_row(static_cast<const T*>(a.q) + ((long long)i * a.Hq + h) * d, d, l8, q);
     const float sl2 = a.scale * kLog2e;
-    State st;
+    State<F> st;
     st.m = -INFINITY;
     st.l = 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) st.o[e] = 0.f;
+    for (int e = 0; e < F; ++e) st.o[e] = 0.f;
     // One step: keys `on` says, their rows at k + at[u] and v + at[u].
     auto step = [&](const auto* k, const auto* v, const long long (&at)[kKeys], const bool (&on)[kKeys],
                     const float (&ks)[kKeys], const float (&vs)[kKeys]) {
         using KT = std::remove_cv_t<std::remove_pointer_t<decltype(k)>>;
-        KT kx[kKeys][16] = {}, vx[kKeys][16] = {};
+        KT kx[kKeys][F] = {}, vx[kKeys][F] = {};
 #pragma unroll
         for (int u = 0; u < kKeys; ++u)
-            if (on[u]) load16(k + at[u], d, l8, kx[u]);
+            if (on[u]) load_row(k + at[u], d, l8, kx[u]);
 #pragma unroll
         for (int u = 0; u < kKeys; ++u)
-            if (on[u]) load16(v + at[u], d, l8, vx[u]);
+            if (on[u]) load_row(v + at[u], d, l8, vx[u]);
         float s[kKeys];
 #pragma unroll
         for (int u = 0; u < kKeys; ++u) {
             s[u] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[u] = fmaf(pg_to_f(q[e]), pg_to_f(kx[u][e]), s[u]);
+            for (int e = 0; e < F; ++e) s[u] = fmaf(pg_to_f(q[e]), pg_to_f(kx[u][e]), s[u]);
         }
         // the eight lanes of a key take part together (their loop bounds are equal)
         const unsigned lanes = 0xffu << (lane & 24);
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_fwd_simt_kernel(const Pa
     st.join_lanes(16);
     if (lane < 8) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) so[warp][32 * (e / 4) + 4 * l8 + e % 4] = st.o[e];
+        for (int e = 0; e < F; ++e) so[warp][32 * (e / 4) + 4 * l8 + e % 4] = st.o[e];
         if (lane == 0) {
             sm[warp] = st.m;
             sl[warp] = st.l;
@@ -184,23 +186,32 @@ __global__ void __launch_bounds__(kMaxWarps * 32) paged_fwd_simt_kernel(const Pa
     if (threadIdx.x == 0 && a.lse) a.lse[(long long)i * a.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+template <typename T, typename KV>
+void launch(const PagedFwdArgs& a, unsigned grid, unsigned th, cudaStream_t s) {
+    if (a.c.d <= 64) paged_fwd_simt_kernel<T, KV, 8><<<grid, th, 0, s>>>(a);
+    else paged_fwd_simt_kernel<T, KV, 16><<<grid, th, 0, s>>>(a);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_fwd_simt(const PagedFwdArgs& a, cudaStream_t s) {
     const PagedCache& c = a.c;
     const long long grid = (long long)c.N * a.Hq;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-    // a warp takes eight keys at a time: up to four rounds before more warps help
+    // a warp takes eight keys at a time: up to four rounds before more warps
+    // help, and no more of them than keep the SMs busy: rows beside each other
+    // hide each other's joins (160 tokens of 8 heads over 1018 keys: 104 us with
+    // 16 warps a row, 84 with two)
     const long long keys = (long long)c.max_blocks * c.page_size;
     int warps = 2;
-    while (warps < kMaxWarps && keys > (long long)warps * 32) warps *= 2;
+    while (warps < kMaxWarps && keys > (long long)warps * 32 && grid * warps < 148 * 16) warps *= 2;
     const unsigned th = warps * 32;
     if (a.dtype == MODA_F32) {
-        if (a.k_scale) paged_fwd_simt_kernel<float, int8_t><<<(unsigned)grid, th, 0, s>>>(a);
-        else paged_fwd_simt_kernel<float, float><<<(unsigned)grid, th, 0, s>>>(a);
+        if (a.k_scale) launch<float, int8_t>(a, (unsigned)grid, th, s);
+        else launch<float, float>(a, (unsigned)grid, th, s);
     } else {
-        if (a.k_scale) paged_fwd_simt_kernel<__nv_bfloat16, int8_t><<<(unsigned)grid, th, 0, s>>>(a);
-        else paged_fwd_simt_kernel<__nv_bfloat16, __nv_bfloat16><<<(unsigned)grid, th, 0, s>>>(a);
+        if (a.k_scale) launch<__nv_bfloat16, int8_t>(a, (unsigned)grid, th, s);
+        else launch<__nv_bfloat16, __nv_bfloat16>(a, (unsigned)grid, th, s);
     }
     return cudaGetLastError();
 }
