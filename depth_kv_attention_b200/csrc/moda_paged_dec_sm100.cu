@@ -25,8 +25,7 @@
 //    what the second product wants as its B operand, once its 8 x 8 blocks are
 //    transposed between lanes (movmatrix).
 //  * 8-bit pages: a lane reads whole 16-byte pieces of a row and turns codes
-//    into bf16 exactly, two at a time ((0x4300 | low 7 bits) is 128 + them, and
-//    (0x4300 | sign bit) is 128 or 256, so one subtraction gives the code). The
+//    into bf16 exactly, two at a time with two instructions (codes_to_bf16). The
 //    order in which a lane holds features is free in a product's contracted
 //    index (queries are laid out alike) and only permutes the output rows.
 //    A key's scale multiplies its logit, a value's scale its P: both exact, as
@@ -147,24 +146,21 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
-// 0x43004300 in a register that the compiler does not see through: with two
-// constants (w & m) | c would be two instructions.
+// 0x00800080 in a register that the compiler does not see through: with two
+// constants (w ^ m) & c would be two instructions.
 __device__ __forceinline__ uint32_t magic_reg() {
     uint32_t r;
-    asm volatile("mov.u32 %0, 0x43004300;" : "=r"(r));
+    asm volatile("mov.u32 %0, 0x00800080;" : "=r"(r));
     return r;
 }
-// Two int8 codes, in bytes 0 and 2 of w, as a bf16 pair (exact).
+// Two int8 codes c, in bytes 0 and 2 of w, as a bf16 pair c / kCodeUnit (exact):
+// the bits 0 .. 255 are the bf16 numbers u 2^-133 (subnormal below 128, one
+// binade above), so u = c + 128 needs one fused multiply-add by 2^127.
+constexpr float kCodeUnit = 64.f;
 __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t w, uint32_t magic) {
-    uint32_t y, base;
-    asm("lop3.b32 %0, %1, 0x007f007f, %2, 0xea;" : "=r"(y) : "r"(w), "r"(magic));     // (w & m) | magic
-    asm("lop3.b32 %0, %1, 0x00800080, %2, 0xea;" : "=r"(base) : "r"(w), "r"(magic));
-    __nv_bfloat162 a, b;
-    memcpy(&a, &y, 4);
-    memcpy(&b, &base, 4);
-    const __nv_bfloat162 r = __hsub2(a, b);
-    uint32_t o;
-    memcpy(&o, &r, 4);
+    uint32_t u, o;
+    asm("lop3.b32 %0, %1, %2, 0x00ff00ff, 0x28;" : "=r"(u) : "r"(w), "r"(magic));  // (w ^ magic) & m
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o) : "r"(u), "r"(0x7f007f00u), "r"(0xc000c000u));
     return o;
 }
 
@@ -686,11 +682,14 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
                         else qk_bf16<NH, NR>(ka + sl * bytes, qf, s[i], lane);
                     }
                 }
-                const float mul = p.sl2 * (Q8 ? ksc : 1.f);
+                const float mul = p.sl2 * (Q8 && seq ? kCodeUnit : 1.f);
 #pragma unroll
                 for (int x = 0; x < NR; ++x)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[i][x][e] *= mul;
+                    for (int e = 0; e < 4; ++e) {
+                        s[i][x][e] *= mul;
+                        if (Q8) s[i][x][e] *= ksc;
+                    }
                 if (!part[i]) {
 #pragma unroll
                     for (int x = 0; x < NR; ++x)
@@ -783,7 +782,8 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
             for (int i = 0; i < C::SL; ++i) {
                 const int sl = wk + i * C::WK;
                 if (!ok || !part[i]) continue;
-                float vsc = 1.f;
+                // (an 8-bit kernel's O is in units of kCodeUnit)
+                float vsc = 1.f / kCodeUnit;
                 if (Q8 && seq) vsc = fmaxf(bars->scale[vslot][sl], 0.f);
                 uint32_t pf[NR][2];
 #pragma unroll
@@ -864,7 +864,7 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
             for (int x = 0; x < NR; ++x) {
                 float inv[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) inv[e] = l[x][e] == 0.f ? 0.f : 1.f / l[x][e];
+                for (int e = 0; e < 2; ++e) inv[e] = l[x][e] == 0.f ? 0.f : (Q8 ? kCodeUnit : 1.f) / l[x][e];
                 if (Q8) {  // 8 NH consecutive features of rows 2t, 2t + 1
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -913,7 +913,8 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
 #pragma unroll
                     for (int n = 0; n < NH * 4; ++n) {
                         if (Q8) {
-                            *reinterpret_cast<float2*>(po + out_col<true, NH>(n, 0, g)) = make_float2(o[x][n][e], o[x][n][2 + e]);
+                            *reinterpret_cast<float2*>(po + out_col<true, NH>(n, 0, g)) =
+                                make_float2(o[x][n][e] * kCodeUnit, o[x][n][2 + e] * kCodeUnit);
                         } else {
                             po[out_col<false, NH>(n, 0, g)] = o[x][n][e];
                             po[out_col<false, NH>(n, 1, g)] = o[x][n][2 + e];
