@@ -7,7 +7,7 @@
 // state and the dual mask). One CTA per (token, query head); eight lanes share
 // a key (four consecutive features of every 32 each), each lane group has two
 // keys in flight and its own running (m, l, o), so a warp works on eight keys
-// at once. Small calls are a chain of loads (48 tokens in four sequences: 6 us);
+// at once. Small calls are a chain of loads (four short sequences, one token each: 6 us);
 // larger ones are bound by instructions, about 50 per key and lane. The states are
 // joined by shuffles within a warp and through shared memory across warps.
 // Only visible keys are touched, so nothing masked can reach a sum.
