@@ -28,8 +28,8 @@
 //    into bf16 exactly, two at a time with two instructions (codes_to_bf16). The
 //    order in which a lane holds features is free in a product's contracted
 //    index (queries are laid out alike) and only permutes the output rows.
-//    A key's scale multiplies its logit, a value's scale its P: both exact, as
-//    scales are powers of two.
+//    A key's scale multiplies its logit, a value's scale its codes or its P
+//    (value_scale): all exact, as scales are powers of two.
 //  * Rounding: logits, P, l, O in fp32; P is rounded to bf16 as the operand of
 //    P V (l sums the unrounded P).
 //  * A value that a row must not see may be anything: a masked P is exactly 0,
@@ -100,7 +100,8 @@ struct Cfg {
 
 struct __align__(8) DecBars {
     uint64_t full[8], empty[8];
-    float scale[8][8];   // per slot and slice: scale (1 for bf16), -1: no page
+    float scale[8][8];   // per slot and slice. Keys: scale (1 for bf16), -1: no page; values: factor of P
+    uint32_t code_mul[8][8];  // 8-bit values: factor of the codes
     float ml[4][16][2];
     long long scan[9];
     long long begin_in_seq;
@@ -157,12 +158,25 @@ __device__ __forceinline__ uint32_t magic_reg() {
 // the bits 0 .. 255 are the bf16 numbers u 2^-133 (subnormal below 128, one
 // binade above), so u = c + 128 needs one fused multiply-add by 2^127.
 constexpr float kCodeUnit = 64.f;
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t w, uint32_t magic) {
+constexpr uint32_t kCodeMul = 0x7f007f00u, kCodeOff = 0xc000c000u;  // 2^127, -2
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t w, uint32_t magic, uint32_t mul = kCodeMul, uint32_t off = kCodeOff) {
     uint32_t u, o;
     asm("lop3.b32 %0, %1, %2, 0x00ff00ff, 0x28;" : "=r"(u) : "r"(w), "r"(magic));  // (w ^ magic) & m
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o) : "r"(u), "r"(0x7f007f00u), "r"(0xc000c000u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(o) : "r"(u), "r"(mul), "r"(off));
     return o;
 }
+// A page's value scale s, 0 or a power of two, as a factor of its codes and one
+// of P, of which one is 1. A scale below one goes to the codes, with the
+// fused multiply-add that converts them anyway (by 2^127 s and -2 s): c s / 64 is
+// exact in bf16 for every s >= 2^-126. As a factor of P it would leave P few bits,
+// or none, where s is small: P s is rounded to bf16, whose step is 2^-133 there.
+// A scale of one and more goes to P. The producer splits the scale (64 sequences
+// up to 8K: 73.0 us, 74.3 with the split in the consumers, 72.3 with all of it on P).
+__device__ __forceinline__ uint32_t code_factor(float s) {  // 2^127 min(s, 1) as a bf16 pair
+    const uint32_t e = __bfloat16_as_ushort(__float2bfloat16_rn(s > 0.f ? fminf(s, 1.f) : 1.f));
+    return (e + (127u << 7)) * 0x10001u;
+}
+__device__ __forceinline__ float p_factor(float s) { return s > 0.f ? fmaxf(s, 1.f) : 0.f; }
 
 // Byte address of feature f of row r of a bf16 slice (64-feature halves of 16
 // rows, 128-byte swizzle).
@@ -219,7 +233,8 @@ __device__ __forceinline__ void qk_q8(uint32_t slice, const uint32_t (&qf)[NR][N
 }
 template <int NH, int NR>
 __device__ __forceinline__ void pv_q8(uint32_t slice, const uint32_t (&pf)[NR][2], float (&o)[NR][NH * 4][4], int lane,
-                                      uint32_t magic) {
+                                      uint32_t magic, uint32_t mul) {
+    const uint32_t off = mul + (kCodeOff - kCodeMul);  // -2 s beside 2^127 s
     const int g = lane >> 2, t = lane & 3;
     uint32_t w[4][NH * 2];  // 8 NH codes of keys 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
@@ -237,10 +252,10 @@ __device__ __forceinline__ void pv_q8(uint32_t slice, const uint32_t (&pf)[NR][2
     for (int m = 0; m < NH * 4; ++m) {
         const int q = m >> 1;
         const uint32_t s0 = (m & 1) ? 0x6622u : 0x4400u, s1 = (m & 1) ? 0x7733u : 0x5511u;  // codes 2m, 2m + 1 of two keys
-        const uint32_t a0 = codes_to_bf16(__byte_perm(w[0][q], w[1][q], s0), magic);
-        const uint32_t a1 = codes_to_bf16(__byte_perm(w[0][q], w[1][q], s1), magic);
-        const uint32_t a2 = codes_to_bf16(__byte_perm(w[2][q], w[3][q], s0), magic);
-        const uint32_t a3 = codes_to_bf16(__byte_perm(w[2][q], w[3][q], s1), magic);
+        const uint32_t a0 = codes_to_bf16(__byte_perm(w[0][q], w[1][q], s0), magic, mul, off);
+        const uint32_t a1 = codes_to_bf16(__byte_perm(w[0][q], w[1][q], s1), magic, mul, off);
+        const uint32_t a2 = codes_to_bf16(__byte_perm(w[2][q], w[3][q], s0), magic, mul, off);
+        const uint32_t a3 = codes_to_bf16(__byte_perm(w[2][q], w[3][q], s1), magic, mul, off);
 #pragma unroll
         for (int x = 0; x < NR; ++x) mma_bf16(o[x][m], a0, a1, a2, a3, pf[x][0], pf[x][1]);
     }
@@ -554,8 +569,10 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
                             const int src = (rel & 31) + (sl & (C::SPS - 1));
                             const int pg = __shfl_sync(0xffffffffu, page, src);
                             const float sc = __shfl_sync(0xffffffffu, kv ? vs : ks, src);
-                            const float none = __shfl_sync(0xffffffffu, ks, src);
-                            if (lane < C::SPS * per_slice && half == 0) bars->scale[slot][sl] = none < 0.f ? -1.f : sc;
+                            if (lane < C::SPS * per_slice && half == 0) {
+                                bars->scale[slot][sl] = Q8 && kv ? p_factor(sc) : sc;
+                                if (Q8 && kv) bars->code_mul[slot][sl] = code_factor(sc);
+                            }
                             __syncwarp();
                             if (lane == 0) ptx::mbar_arrive_expect_tx(bar, C::kSlot);
                             __syncwarp();
@@ -784,7 +801,7 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
                 if (!ok || !part[i]) continue;
                 // (an 8-bit kernel's O is in units of kCodeUnit)
                 float vsc = 1.f / kCodeUnit;
-                if (Q8 && seq) vsc = fmaxf(bars->scale[vslot][sl], 0.f);
+                if (Q8 && seq) vsc = bars->scale[vslot][sl];
                 uint32_t pf[NR][2];
 #pragma unroll
                 for (int x = 0; x < NR; ++x)
@@ -793,7 +810,7 @@ __global__ void __launch_bounds__(Cfg<Q8, NH, NR, WR>::kThreads, Cfg<Q8, NH, NR,
                         pf[x][h] = transpose8x8(Q8 ? ptx::pack_bf16x2(s[i][x][2 * h] * vsc, s[i][x][2 * h + 1] * vsc)
                                                    : ptx::pack_bf16x2(s[i][x][2 * h], s[i][x][2 * h + 1]));
                 if (seq) {
-                    if (Q8) pv_q8<NH, NR>(va + sl * bytes, pf, o, lane, magic);
+                    if (Q8) pv_q8<NH, NR>(va + sl * bytes, pf, o, lane, magic, bars->code_mul[vslot][sl]);
                     else pv_bf16<NH, NR>(va + sl * bytes, pf, o, lane);
                 } else {
                     if (Q8) pv_bf16_perm<NH, NR>(va + sl * bytes, pf, o, lane);
