@@ -5,7 +5,8 @@ pointers and the current CUDA stream to the C entry point of the same name
 (the paged-cache functions through a compiled binding, the others by ctypes).
 All arithmetic runs in the library's CUDA kernels. There is no CPU fallback:
 importing this package fails if the library has not been built
-(``python depth_kv_attention_b200/csrc/build.py``).
+(``python depth_kv_attention_b200/csrc/build.py``); without the binding the
+paged-cache functions raise ImportError.
 
 Layouts (contiguous): q/out/dout [B,T,Hq,d]; k/v [B,T,Hkv,d];
 kd/vd [B,T,Ld,Hkv,d]; lse [B,Hq,T] fp32. The paged sequence cache packs the
@@ -36,11 +37,7 @@ if not os.path.exists(LIB_PATH):
         f"{LIB_PATH} is missing: build it with `python depth_kv_attention_b200/csrc/build.py` "
         "(the MoDA path has no CPU fallback)")
 lib = ctypes.CDLL(LIB_PATH)
-try:
-    from . import _moda_torch as _bind  # the paged-cache entry points on tensors
-except ImportError as e:
-    raise ImportError(f"depth_kv_attention_b200/_moda_torch.so does not load ({e}): build it with "
-                      "`python depth_kv_attention_b200/csrc/build.py`") from e
+_bind = None  # the compiled binding of the paged-cache functions, once one is called
 
 MODA_OK = 0
 _DTYPE = {torch.bfloat16: 0, torch.float32: 1}
@@ -386,6 +383,20 @@ def depth_slot_view(kd, slot: int):
     return kd.as_strided((B, T, Hkv, d), st, kd.storage_offset() + off)
 
 
+def _binding():
+    """The compiled binding. It needs torch's C++ headers to build, which the
+    rest of the package does without."""
+    global _bind
+    if _bind is None:
+        try:
+            from . import _moda_torch
+        except ImportError as e:
+            raise ImportError(f"depth_kv_attention_b200/_moda_torch.so does not load ({e}): build it with "
+                              "`python depth_kv_attention_b200/csrc/build.py`") from e
+        _bind = _moda_torch
+    return _bind
+
+
 def _result(r, where):
     """A binding function's result; a status code becomes a ModaError."""
     if type(r) is int:
@@ -406,8 +417,8 @@ def moda_paged_append(q, k, v, k_pages, v_pages, block_table, cu_q, ctx_lens, ro
     column blocks of one projection's output serve as they are. ``rope``
     [positions, rot_dim] holds cos | sin rows; None leaves q and k unrotated.
     Returns the rotated q (``q_out`` when given; None without q)."""
-    return _result(_bind.paged_append(q, k, v, k_pages, v_pages, None, None, block_table, cu_q, ctx_lens, rope,
-                                      interleaved, q_out, kd, vd, slot, _handle(stream)), "moda_paged_append")
+    return _result(_binding().paged_append(q, k, v, k_pages, v_pages, None, None, block_table, cu_q, ctx_lens, rope,
+                                           interleaved, q_out, kd, vd, slot, _handle(stream)), "moda_paged_append")
 
 
 def moda_paged_append_q8(q, k, v, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens, rope=None,
@@ -417,8 +428,9 @@ def moda_paged_append_q8(q, k, v, k_pages, v_pages, k_scale, v_scale, block_tabl
     place. kd, vd stay in the tokens' type."""
     if k_scale is None or v_scale is None:
         raise ValueError("moda_paged_append_q8: fp32 scales [num_pages,Hkv] expected")
-    return _result(_bind.paged_append(q, k, v, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens, rope,
-                                      interleaved, q_out, kd, vd, slot, _handle(stream)), "moda_paged_append_q8")
+    return _result(_binding().paged_append(q, k, v, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens,
+                                           rope, interleaved, q_out, kd, vd, slot, _handle(stream)),
+                   "moda_paged_append_q8")
 
 
 def moda_fwd_paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, num_pages, page_size, dtype, q8: bool = False) -> int:
@@ -434,8 +446,8 @@ def moda_fwd_paged(q, k_pages, v_pages, block_table, cu_q, ctx_lens, max_q: int,
     [N,slots,Hkv,d]. ``max_q``: about the most new tokens of any sequence.
     ``workspace``: a CUDA tensor of moda_fwd_paged_workspace_bytes bytes, made
     here when not given. Returns (out [N,Hq,d], lse [N,Hq])."""
-    return _result(_bind.fwd_paged(q, k_pages, v_pages, None, None, block_table, cu_q, ctx_lens, max_q, kd, vd, Ld, scale,
-                                   out, lse, workspace, _IMPL[impl], _handle(stream)), "moda_fwd_paged")
+    return _result(_binding().fwd_paged(q, k_pages, v_pages, None, None, block_table, cu_q, ctx_lens, max_q, kd, vd, Ld,
+                                        scale, out, lse, workspace, _IMPL[impl], _handle(stream)), "moda_fwd_paged")
 
 
 def moda_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens, max_q: int, kd=None,
@@ -445,8 +457,9 @@ def moda_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, 
     and fp32 scales [num_pages,Hkv], as moda_paged_append_q8 writes them."""
     if k_scale is None or v_scale is None:
         raise ValueError("moda_fwd_paged_q8: fp32 scales [num_pages,Hkv] expected")
-    return _result(_bind.fwd_paged(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens, max_q, kd, vd, Ld,
-                                   scale, out, lse, workspace, _IMPL[impl], _handle(stream)), "moda_fwd_paged_q8")
+    return _result(_binding().fwd_paged(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens, max_q, kd,
+                                        vd, Ld, scale, out, lse, workspace, _IMPL[impl], _handle(stream)),
+                   "moda_fwd_paged_q8")
 
 
 def moda_device_status(stream=None) -> int:
