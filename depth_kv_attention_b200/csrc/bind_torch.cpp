@@ -272,4 +272,12 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_moda_torch", nullptr, -1, kMetho
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject* PyInit__moda_torch(void) { return PyModule_Create(&kModule); }
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit__moda_torch(void) {
+    PyObject* m = PyModule_Create(&kModule);
+    // the torch that this was compiled against: tensors of another one may be laid out differently
+    if (m && PyModule_AddStringConstant(m, "torch_version", MODA_TORCH_VERSION) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -35,3 +35,66 @@ for call in (lambda: moda.moda_paged_append(z, z, z, z, z, z, z, z), lambda: mod
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr + r.stdout
+
+
+def build_module():
+    spec = importlib.util.spec_from_file_location(
+        "moda_build_under_test", os.path.join(ROOT, "depth_kv_attention_b200", "csrc", "build.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+def test_binding_is_built_again_when_torch_changes(tmp_path, monkeypatch):
+    """The object depends on the installed torch and Python and on the compile
+    command as much as on its source."""
+    mod = build_module()
+    monkeypatch.setattr(mod, "BIND", str(tmp_path / "_moda_torch.so"))
+    monkeypatch.setattr(mod, "BUILD", str(tmp_path / "_build"))
+    runs = []
+
+    def compile_(cmd, **kw):
+        runs.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("object")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(mod.subprocess, "run", compile_)
+    mod.build_binding()
+    mod.build_binding()
+    assert len(runs) == 1
+    with monkeypatch.context() as m:
+        m.setattr("importlib.metadata.version", lambda name: "99.0")
+        mod.build_binding()
+        mod.build_binding()
+    assert len(runs) == 2
+    with monkeypatch.context() as m:
+        m.setattr("sysconfig.get_config_var", lambda name: ".other-python.so")
+        mod.build_binding()
+    assert len(runs) == 3
+    mod.build_binding(force=True)
+    assert len(runs) == 4
+    os.remove(mod.BIND)
+    mod.build_binding()
+    assert len(runs) == 5
+
+
+def test_a_failed_compile_leaves_no_key(tmp_path, monkeypatch):
+    mod = build_module()
+    monkeypatch.setattr(mod, "BIND", str(tmp_path / "_moda_torch.so"))
+    monkeypatch.setattr(mod, "BUILD", str(tmp_path / "_build"))
+    monkeypatch.setattr(mod.subprocess, "run", lambda cmd, **kw: subprocess.CompletedProcess(cmd, 1, "", "no header"))
+    for _ in range(2):
+        with pytest.raises(RuntimeError, match="no header"):
+            mod.build_binding()
+
+
+def test_binding_of_another_torch_is_refused(monkeypatch):
+    import torch
+
+    import depth_kv_attention_b200 as moda
+    monkeypatch.setattr(moda, "_bind", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    z = torch.zeros(1)
+    with pytest.raises(ImportError, match="0.0.1"):
+        moda.moda_fwd_paged(z, z, z, z, z, z, 1)
