@@ -5,7 +5,9 @@
 //
 // The functions take positional arguments only (the package's functions of the
 // same names hold the signatures and documentation) and return the result, or a
-// non-zero status code as an int. A wrong argument raises ValueError.
+// non-zero status code as an int. A wrong argument raises ValueError; torch's
+// errors (an allocation that fails) come as torch's own types.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
@@ -115,12 +117,8 @@ PyObject* guarded(F&& f) {
         return f();
     } catch (const std::invalid_argument& e) {
         PyErr_SetString(PyExc_ValueError, e.what());
-    } catch (const c10::OutOfMemoryError& e) {
-        PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
-    } catch (const c10::Error& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {  // as torch's own functions: torch.OutOfMemoryError and the like
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

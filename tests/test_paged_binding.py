@@ -98,3 +98,28 @@ def test_binding_of_another_torch_is_refused(monkeypatch):
     z = torch.zeros(1)
     with pytest.raises(ImportError, match="0.0.1"):
         moda.moda_fwd_paged(z, z, z, z, z, z, 1)
+
+
+@pytest.mark.gpu
+def test_out_of_memory_is_torchs():
+    """An allocation that fails raises what torch's own functions raise."""
+    import torch
+
+    import depth_kv_attention_b200 as moda
+
+    def z(*s, t=torch.bfloat16):
+        return torch.zeros(s, dtype=t, device="cuda")
+
+    q, kp, table = z(4096, 32, 128), z(8, 4, 16, 128), z(1, 8, t=torch.int32)
+    k = z(4096, 4, 128)
+    cu, ctx = torch.tensor([0, 4096], dtype=torch.int32).cuda(), torch.tensor([128], dtype=torch.int32).cuda()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(0.0)  # the allocator takes nothing more from the driver
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            moda.moda_fwd_paged(q, kp, kp, table, cu, ctx, 4096)
+        with pytest.raises(torch.OutOfMemoryError):
+            moda.moda_paged_append(q, k, k, kp, kp, table, cu, ctx)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
