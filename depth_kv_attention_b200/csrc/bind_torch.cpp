@@ -136,6 +136,10 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensor *rope = tensor(a[10], where, true), *qo = tensor(a[12], where, true);
         const Tensor *kd = tensor(a[13], where, true), *vd = tensor(a[14], where, true);
         const int inter = PyObject_IsTrue(a[11]);
+        if (inter < 0) {
+            PyErr_Clear();
+            bad(where, "a truth value expected as interleaved");
+        }
         const long long slot = integer(a[15], where);
         if (slot < 0 || slot > 0x7fffffffLL) bad(where, "slot must lie in [0, slots of kd)");
         Cache c = check_cache(where, *k, *kp, *vp, ks, vs, *table, *cu, *ctx, kd, vd, {rope, qo});

@@ -100,6 +100,16 @@ def test_binding_of_another_torch_is_refused(monkeypatch):
         moda.moda_fwd_paged(z, z, z, z, z, z, 1)
 
 
+def test_a_flag_without_a_truth_value_is_refused():
+    """Before anything runs, and not as a result with an error pending."""
+    import torch
+
+    import depth_kv_attention_b200 as moda
+    z = torch.zeros(1)
+    with pytest.raises(ValueError, match="interleaved"):
+        moda.moda_paged_append(z, z, z, z, z, z, z, z, interleaved=torch.zeros(2))
+
+
 @pytest.mark.gpu
 def test_out_of_memory_is_torchs():
     """An allocation that fails raises what torch's own functions raise."""
