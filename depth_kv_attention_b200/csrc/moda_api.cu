@@ -3,6 +3,7 @@
 // synchronisation (except moda_device_status, and moda_fwd_host's own
 // streams and events), no state beyond the device status word and the test
 // hook's wait limit.
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cstring>
@@ -577,6 +578,23 @@ moda_status run_append(const void* q, const void* k, const void* v, long long sq
     return launch_paged_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MODA_OK : MODA_ERR_LAUNCH;
 }
 
+// The kernel of a call, and the workspace it needs. Both the size functions and
+// the calls ask here.
+enum class PagedKernel { Simt, Dec, Pre };
+
+PagedKernel paged_kernel(const PagedFwdArgs& a, moda_impl impl) {
+    if (impl == MODA_IMPL_SIMT || !paged_dec_supported(a)) return PagedKernel::Simt;
+    return (long long)a.max_q * a.G >= kPagedPreRows && paged_pre_supported(a) ? PagedKernel::Pre : PagedKernel::Dec;
+}
+
+size_t paged_workspace(const PagedFwdArgs& a, PagedKernel k) {
+    switch (k) {
+        case PagedKernel::Simt: return 0;
+        case PagedKernel::Dec: return paged_dec_workspace(a.max_q, a.G, a.c.d);
+        default: return paged_pre_workspace(a.c.Hkv, a.c.d, a.c.num_pages, a.c.page_size, a.k_scale != nullptr);
+    }
+}
+
 moda_status run_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
                           const float* v_scale, const void* kd, const void* vd, const int32_t* cu_q,
                           const int32_t* ctx_lens, const int32_t* block_table, int N, int B, int max_q, int Hq,
@@ -596,20 +614,19 @@ moda_status run_fwd_paged(const void* q, const void* k_pages, const void* v_page
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned4(lse) ||
         !aligned4(k_scale) || !aligned4(v_scale) || (Ld > 0 && (!aligned16(kd) || !aligned16(vd))))
         return MODA_ERR_MISALIGNED;
-    const size_t need = moda_fwd_paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, num_pages, page_size, dtype, k_scale != nullptr);
-    if (need && (!workspace || workspace_bytes < need)) return MODA_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return MODA_ERR_MISALIGNED;
     a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.k_scale = k_scale; a.v_scale = v_scale;
     a.kd = kd; a.vd = vd; a.Hq = Hq; a.G = Hq / Hkv; a.Ld = Ld; a.Ld_cap = Ld_cap; a.max_q = max_q;
     a.scale = scale; a.dtype = dtype; a.out = out; a.lse = lse; a.workspace = workspace;
-    const bool tc_ok = paged_dec_supported(a);
-    if (impl == MODA_IMPL_TC2 || (impl == MODA_IMPL_TC && !tc_ok)) return MODA_ERR_UNSUPPORTED;
+    const PagedKernel kernel = paged_kernel(a, impl);
+    const size_t need = paged_workspace(a, kernel);
+    if (need && (!workspace || workspace_bytes < need)) return MODA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MODA_ERR_MISALIGNED;
+    if (impl == MODA_IMPL_TC2 || (impl == MODA_IMPL_TC && kernel == PagedKernel::Simt)) return MODA_ERR_UNSUPPORTED;
     if (status_ptr(&a.status, &a.wait_limit) != cudaSuccess) return MODA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (!tc_ok || impl == MODA_IMPL_SIMT) e = launch_paged_fwd_simt(a, s);
-    else if ((long long)max_q * a.G >= kPagedPreRows && paged_pre_supported(a)) e = launch_paged_pre(a, s);
-    else e = launch_paged_dec(a, s);
+    const cudaError_t e = kernel == PagedKernel::Simt  ? launch_paged_fwd_simt(a, s)
+                          : kernel == PagedKernel::Pre ? launch_paged_pre(a, s)
+                                                       : launch_paged_dec(a, s);
     return e == cudaSuccess ? MODA_OK : MODA_ERR_LAUNCH;
 }
 
@@ -642,11 +659,18 @@ size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, 
                                       moda_dtype dtype, int q8) {
     if (N < 1 || B < 1 || max_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1 || d > 128 || num_pages < 1 || page_size < 1)
         return 0;
-    if (dtype != MODA_BF16 || page_size % 16) return 0;
-    const size_t dec = paged_dec_workspace(max_q, Hq / Hkv, d);
-    if ((long long)max_q * (Hq / Hkv) < kPagedPreRows || Hq / Hkv > 128) return dec;
-    const size_t pre = paged_pre_workspace(Hkv, d, num_pages, page_size, q8 != 0);
-    return pre > dec ? pre : dec;
+    PagedFwdArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.c.N = N; a.c.B = B; a.c.Hkv = Hkv; a.c.d = d; a.c.num_pages = num_pages; a.c.page_size = page_size;
+    a.Hq = Hq; a.G = Hq / Hkv; a.max_q = max_q; a.dtype = dtype;
+    const float is_q8 = 1.f;
+    a.k_scale = q8 ? &is_q8 : nullptr;
+    size_t most = 0;
+    for (const float scale : {0.f, 1.f}) {  // not known here, and one of 0 and below may take another kernel
+        a.scale = scale;
+        most = std::max(most, paged_workspace(a, paged_kernel(a, MODA_IMPL_AUTO)));
+    }
+    return most;
 }
 
 moda_status moda_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* kd, const void* vd,
