@@ -78,6 +78,7 @@ _c_quant_q8 = _sig("moda_depth_quantize_q8", _i, [_vp, _vp] + [_i] * 5 + [_i] + 
 _c_write_q8 = _sig("moda_depth_write_q8", _i, [_vp, _vp] + [_i] * 6 + [_i] + [_vp] * 4 + [_vp])
 _c_fwd_host = _sig("moda_fwd_host", _i, [_vp] * 5 + _DIMS + [_i, _f, _vp, _vp, _vp, _sz, _vp])
 _c_paged_ws = _sig("moda_fwd_paged_workspace_bytes", _sz, [_i] * 10)
+_c_paged_ws_ex = _sig("moda_fwd_paged_workspace_bytes_ex", _sz, [_i] * 12)
 
 
 class ModaError(RuntimeError):
@@ -436,8 +437,14 @@ def moda_paged_append_q8(q, k, v, k_pages, v_pages, k_scale, v_scale, block_tabl
                    "moda_paged_append_q8")
 
 
-def moda_fwd_paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, num_pages, page_size, dtype, q8: bool = False) -> int:
-    return _c_paged_ws(N, B, max_q, Hq, Hkv, d, num_pages, page_size, _DTYPE[dtype], int(q8))
+def moda_fwd_paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, num_pages, page_size, dtype, q8: bool = False,
+                                   max_blocks: int | None = None, impl: str = "auto") -> int:
+    """Workspace of a paged attention call. With ``max_blocks`` (the block
+    table's width) chunks over 8-bit pages need room for the call's pages only,
+    not for the whole cache's (``moda_fwd_paged_workspace_bytes_ex``)."""
+    if max_blocks is None:
+        return _c_paged_ws(N, B, max_q, Hq, Hkv, d, num_pages, page_size, _DTYPE[dtype], int(q8))
+    return _c_paged_ws_ex(N, B, max_q, Hq, Hkv, d, num_pages, page_size, max_blocks, _DTYPE[dtype], int(q8), _IMPL[impl])
 
 
 def moda_fwd_paged(q, k_pages, v_pages, block_table, cu_q, ctx_lens, max_q: int, kd=None, vd=None,
@@ -456,8 +463,11 @@ def moda_fwd_paged(q, k_pages, v_pages, block_table, cu_q, ctx_lens, max_q: int,
 def moda_fwd_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens, max_q: int, kd=None,
                       vd=None, Ld: int | None = None, scale: float | None = None, out=None, lse=None, workspace=None,
                       impl: str = "auto", stream=None):
-    """``moda_fwd_paged`` over 8-bit pages (``moda_fwd_paged_q8``): int8 codes
-    and fp32 scales [num_pages,Hkv], as moda_paged_append_q8 writes them."""
+    """``moda_fwd_paged`` over 8-bit pages (``moda_fwd_paged_q8_ex``): int8 codes
+    and fp32 scales [num_pages,Hkv], as moda_paged_append_q8 writes them. A chunk
+    turns its pages into bf16 in the workspace; with one made or given for
+    q8=False, or where no more memory is to be had, it takes the kernel for few
+    rows instead, which is slower there."""
     if k_scale is None or v_scale is None:
         raise ValueError("moda_fwd_paged_q8: fp32 scales [num_pages,Hkv] expected")
     return _result(_binding().fwd_paged(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_q, ctx_lens, max_q, kd,

@@ -229,21 +229,32 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         moda_status st = MODA_OK;
         if (c.N > 0) {
-            const size_t need = moda_fwd_paged_workspace_bytes(c.N, c.B, max_q, c.Hq, c.Hkv, c.d, c.pages, c.page, c.dt, q8);
-            if (!ws && need) {
+            const moda_impl impl = (moda_impl)integer(a[16], where);
+            auto make_ws = [&](int copy) {
+                const size_t need = moda_fwd_paged_workspace_bytes_ex(c.N, c.B, max_q, c.Hq, c.Hkv, c.d, c.pages, c.page,
+                                                                      c.blocks, c.dt, copy, impl);
+                if (!need) return;
                 made_ws = at::empty({(int64_t)need}, q->options().dtype(at::kByte));
                 ws = &made_ws;
+            };
+            if (!ws) {
+                try {
+                    make_ws(q8);
+                } catch (const c10::OutOfMemoryError&) {
+                    if (!q8) throw;
+                    make_ws(0);  // without the bf16 copy of 8-bit pages
+                }
             }
             const size_t have = ws ? ws->nbytes() : 0;
-            const moda_impl impl = (moda_impl)integer(a[16], where);
             void* s = stream.stream();
             auto i32 = [](const Tensor* t) { return static_cast<const int32_t*>(t->data_ptr()); };
             const void *kda = Ld ? addr(kd) : nullptr, *vda = Ld ? addr(vd) : nullptr;
             float* lp = static_cast<float*>(addr(lse));
-            st = q8 ? moda_fwd_paged_q8(addr(q), static_cast<const int8_t*>(addr(kp)), static_cast<const int8_t*>(addr(vp)),
-                                        static_cast<const float*>(addr(ks)), static_cast<const float*>(addr(vs)), kda, vda, i32(cu),
-                                        i32(ctx), i32(table), c.N, c.B, max_q, c.Hq, c.Hkv, c.d, (int)Ld, cap, c.pages, c.page,
-                                        c.blocks, c.dt, (float)scale, addr(out), lp, addr(ws), have, s, impl)
+            st = q8 ? moda_fwd_paged_q8_ex(addr(q), static_cast<const int8_t*>(addr(kp)), static_cast<const int8_t*>(addr(vp)),
+                                           static_cast<const float*>(addr(ks)), static_cast<const float*>(addr(vs)), kda, vda,
+                                           i32(cu), i32(ctx), i32(table), c.N, c.B, max_q, c.Hq, c.Hkv, c.d, (int)Ld, cap,
+                                           c.pages, c.page, c.blocks, c.dt, (float)scale, addr(out), lp, addr(ws), have, s,
+                                           impl)
                     : moda_fwd_paged(addr(q), addr(kp), addr(vp), kda, vda, i32(cu), i32(ctx), i32(table), c.N, c.B, max_q, c.Hq,
                                      c.Hkv, c.d, (int)Ld, cap, c.pages, c.page, c.blocks, c.dt, (float)scale, addr(out), lp,
                                      addr(ws), have, s, impl);

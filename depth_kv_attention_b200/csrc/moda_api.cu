@@ -591,8 +591,28 @@ size_t paged_workspace(const PagedFwdArgs& a, PagedKernel k) {
     switch (k) {
         case PagedKernel::Simt: return 0;
         case PagedKernel::Dec: return paged_dec_workspace(a.max_q, a.G, a.c.d);
-        default: return paged_pre_workspace(a.c.Hkv, a.c.d, a.c.num_pages, a.c.page_size, a.k_scale != nullptr);
+        default: return paged_pre_workspace(a.c, a.k_scale != nullptr);
     }
+}
+
+// max_blocks == 0: not known.
+size_t paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d, int num_pages, int page_size,
+                             int max_blocks, moda_dtype dtype, int q8, moda_impl impl) {
+    if (N < 1 || B < 1 || max_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1 || d > 128 || num_pages < 1 || page_size < 1)
+        return 0;
+    PagedFwdArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.c.N = N; a.c.B = B; a.c.Hkv = Hkv; a.c.d = d;
+    a.c.num_pages = num_pages; a.c.page_size = page_size; a.c.max_blocks = max_blocks;
+    a.Hq = Hq; a.G = Hq / Hkv; a.max_q = max_q; a.dtype = dtype;
+    const float is_q8 = 1.f;
+    a.k_scale = q8 ? &is_q8 : nullptr;
+    size_t most = 0;
+    for (const float scale : {0.f, 1.f}) {  // not known here, and one of 0 and below may take another kernel
+        a.scale = scale;
+        most = std::max(most, paged_workspace(a, paged_kernel(a, impl)));
+    }
+    return most;
 }
 
 moda_status run_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
@@ -600,7 +620,7 @@ moda_status run_fwd_paged(const void* q, const void* k_pages, const void* v_page
                           const int32_t* ctx_lens, const int32_t* block_table, int N, int B, int max_q, int Hq,
                           int Hkv, int d, int Ld, int Ld_cap, int num_pages, int page_size, int max_blocks,
                           moda_dtype dtype, float scale, void* out, float* lse, void* workspace,
-                          size_t workspace_bytes, void* stream, moda_impl impl) {
+                          size_t workspace_bytes, void* stream, moda_impl impl, bool by_call) {
     if (impl != MODA_IMPL_AUTO && impl != MODA_IMPL_SIMT && impl != MODA_IMPL_TC && impl != MODA_IMPL_TC2)
         return MODA_ERR_INVALID_VALUE;
     PagedFwdArgs a;
@@ -617,8 +637,14 @@ moda_status run_fwd_paged(const void* q, const void* k_pages, const void* v_page
     a.q = q; a.k_pages = k_pages; a.v_pages = v_pages; a.k_scale = k_scale; a.v_scale = v_scale;
     a.kd = kd; a.vd = vd; a.Hq = Hq; a.G = Hq / Hkv; a.Ld = Ld; a.Ld_cap = Ld_cap; a.max_q = max_q;
     a.scale = scale; a.dtype = dtype; a.out = out; a.lse = lse; a.workspace = workspace;
-    const PagedKernel kernel = paged_kernel(a, impl);
-    const size_t need = paged_workspace(a, kernel);
+    PagedKernel kernel = paged_kernel(a, impl);
+    PagedFwdArgs sized = a;
+    if (!by_call) sized.c.max_blocks = 0;
+    size_t need = paged_workspace(sized, kernel);
+    if (by_call && k_scale && kernel == PagedKernel::Pre && workspace_bytes < need) {
+        kernel = PagedKernel::Dec;  // reads 8-bit pages as they are
+        need = paged_workspace(a, kernel);
+    }
     if (need && (!workspace || workspace_bytes < need)) return MODA_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MODA_ERR_MISALIGNED;
     if (impl == MODA_IMPL_TC2 || (impl == MODA_IMPL_TC && kernel == PagedKernel::Simt)) return MODA_ERR_UNSUPPORTED;
@@ -657,20 +683,13 @@ moda_status moda_paged_append_q8(const void* q, const void* k, const void* v, lo
 
 size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d, int num_pages, int page_size,
                                       moda_dtype dtype, int q8) {
-    if (N < 1 || B < 1 || max_q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || d < 1 || d > 128 || num_pages < 1 || page_size < 1)
-        return 0;
-    PagedFwdArgs a;
-    std::memset(&a, 0, sizeof(a));
-    a.c.N = N; a.c.B = B; a.c.Hkv = Hkv; a.c.d = d; a.c.num_pages = num_pages; a.c.page_size = page_size;
-    a.Hq = Hq; a.G = Hq / Hkv; a.max_q = max_q; a.dtype = dtype;
-    const float is_q8 = 1.f;
-    a.k_scale = q8 ? &is_q8 : nullptr;
-    size_t most = 0;
-    for (const float scale : {0.f, 1.f}) {  // not known here, and one of 0 and below may take another kernel
-        a.scale = scale;
-        most = std::max(most, paged_workspace(a, paged_kernel(a, MODA_IMPL_AUTO)));
-    }
-    return most;
+    return paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, num_pages, page_size, 0, dtype, q8, MODA_IMPL_AUTO);
+}
+
+size_t moda_fwd_paged_workspace_bytes_ex(int N, int B, int max_q, int Hq, int Hkv, int d, int num_pages, int page_size,
+                                         int max_blocks, moda_dtype dtype, int q8, moda_impl impl) {
+    if (max_blocks < 1) return 0;
+    return paged_workspace_bytes(N, B, max_q, Hq, Hkv, d, num_pages, page_size, max_blocks, dtype, q8, impl);
 }
 
 moda_status moda_fwd_paged(const void* q, const void* k_pages, const void* v_pages, const void* kd, const void* vd,
@@ -680,7 +699,7 @@ moda_status moda_fwd_paged(const void* q, const void* k_pages, const void* v_pag
                            size_t workspace_bytes, void* stream, moda_impl impl) {
     return run_fwd_paged(q, k_pages, v_pages, nullptr, nullptr, kd, vd, cu_q, ctx_lens, block_table, N, B, max_q, Hq,
                          Hkv, d, Ld, Ld_cap, num_pages, page_size, max_blocks, dtype, scale, out, lse, workspace,
-                         workspace_bytes, stream, impl);
+                         workspace_bytes, stream, impl, false);
 }
 
 moda_status moda_fwd_paged_q8(const void* q, const int8_t* k_pages, const int8_t* v_pages, const float* k_scale,
@@ -692,7 +711,19 @@ moda_status moda_fwd_paged_q8(const void* q, const int8_t* k_pages, const int8_t
     if (!k_scale || !v_scale) return MODA_ERR_INVALID_VALUE;
     return run_fwd_paged(q, k_pages, v_pages, k_scale, v_scale, kd, vd, cu_q, ctx_lens, block_table, N, B, max_q, Hq,
                          Hkv, d, Ld, Ld_cap, num_pages, page_size, max_blocks, dtype, scale, out, lse, workspace,
-                         workspace_bytes, stream, impl);
+                         workspace_bytes, stream, impl, false);
+}
+
+moda_status moda_fwd_paged_q8_ex(const void* q, const int8_t* k_pages, const int8_t* v_pages, const float* k_scale,
+                                 const float* v_scale, const void* kd, const void* vd, const int32_t* cu_q,
+                                 const int32_t* ctx_lens, const int32_t* block_table, int N, int B, int max_q, int Hq,
+                                 int Hkv, int d, int Ld, int Ld_cap, int num_pages, int page_size, int max_blocks,
+                                 moda_dtype dtype, float scale, void* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream, moda_impl impl) {
+    if (!k_scale || !v_scale) return MODA_ERR_INVALID_VALUE;
+    return run_fwd_paged(q, k_pages, v_pages, k_scale, v_scale, kd, vd, cu_q, ctx_lens, block_table, N, B, max_q, Hq,
+                         Hkv, d, Ld, Ld_cap, num_pages, page_size, max_blocks, dtype, scale, out, lse, workspace,
+                         workspace_bytes, stream, impl, true);
 }
 
 moda_status moda_device_status(void* stream) {

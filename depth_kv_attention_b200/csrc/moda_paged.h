@@ -70,7 +70,7 @@ size_t paged_dec_workspace(int max_q, int G, int d);
 cudaError_t launch_paged_dec(const PagedFwdArgs& a, cudaStream_t s);
 // tcgen05 attention for many rows per sequence (moda_paged_pre_sm100.cu).
 bool paged_pre_supported(const PagedFwdArgs& a);
-size_t paged_pre_workspace(int Hkv, int d, long long num_pages, int page_size, bool q8);
+size_t paged_pre_workspace(const PagedCache& c, bool q8);  // c.max_blocks may be 0: not known
 cudaError_t launch_paged_pre(const PagedFwdArgs& a, cudaStream_t s);
 // Rows per sequence and kv-head from which it is the one that runs. 48
 // sequences of 3000 tokens, 33 to 40 rows: G = 8 78 us against 116 on the other

@@ -1038,16 +1038,18 @@ cudaError_t launch(const PagedFwdArgs& a, char* ws, cudaStream_t s) {
     return a.c.d <= 64 ? launch_halves<1>(a, ws, s) : launch_halves<2>(a, ws, s);
 }
 
-// 8-bit pages to bf16 pages of the same numbering, for the pages this call
+// 8-bit pages to bf16 pages, for the pages this call
 // reads: value = code * scale, exact, as the scale is a power of two. Every
 // unit of a chunk would otherwise convert the same tiles again: in the kernel
 // the conversion shared the SM with the softmax and took two and a half times
 // the matrix products' time, here it is one pass over the cache (1 byte read,
 // 2 written per element), and what it writes is still in L2 when it is read.
 // One CTA per (block of the table, kv-head): 16 codes per thread and step.
+// The copies have the pages' own numbers, or, with `table`, those of the block
+// table's entries, which then names them for the attention.
 __global__ void __launch_bounds__(256) paged_dequant_kernel(const PagedCache c, const int8_t* kc, const int8_t* vc,
                                                             const float* ks, const float* vs, __nv_bfloat16* ko,
-                                                            __nv_bfloat16* vo) {
+                                                            __nv_bfloat16* vo, int32_t* table) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int h = blockIdx.y;
     const int total = c.B * c.max_blocks;
@@ -1055,12 +1057,13 @@ __global__ void __launch_bounds__(256) paged_dequant_kernel(const PagedCache c, 
         const int b = x / c.max_blocks, blk = x % c.max_blocks;
         const SeqInfo s = seq_info(c, b);
         const long long keys = (long long)s.pos0 + s.n;  // seen by the last new token
-        if (s.n == 0 || (long long)blk * c.page_size >= keys) continue;
-        const int page = page_of(c, b, blk);
+        const bool seen = s.n != 0 && (long long)blk * c.page_size < keys;
+        const int page = seen ? page_of(c, b, blk) : -1;
+        if (table && h == 0 && threadIdx.x == 0) table[x] = page < 0 ? -1 : x;
         if (page < 0) continue;
-        const long long row = (long long)page * c.Hkv + h;
+        const long long row = (long long)page * c.Hkv + h, to_row = table ? (long long)x * c.Hkv + h : row;
         const float k1 = __ldg(ks + row), v1 = __ldg(vs + row);
-        const long long at = row * c.page_size * c.d;
+        const long long at = row * c.page_size * c.d, to = to_row * c.page_size * c.d;
         const int n16 = (int)min((long long)c.page_size, keys - (long long)blk * c.page_size) * (c.d / 16);
         for (int e = threadIdx.x; e < n16; e += blockDim.x) {
             const uint4 a = *reinterpret_cast<const uint4*>(kc + at + e * 16), d = *reinterpret_cast<const uint4*>(vc + at + e * 16);
@@ -1075,8 +1078,8 @@ __global__ void __launch_bounds__(256) paged_dequant_kernel(const PagedCache c, 
                 }
                 ptx::st_global_32b(dst, o);
             };
-            put(a, k1, ko + at + e * 16);
-            put(d, v1, vo + at + e * 16);
+            put(a, k1, ko + to + e * 16);
+            put(d, v1, vo + to + e * 16);
         }
     }
 }
@@ -1084,8 +1087,26 @@ __global__ void __launch_bounds__(256) paged_dequant_kernel(const PagedCache c, 
 size_t join_bytes() {
     return kParts * sizeof(int4) + 2 * (size_t)kParts * kRows * (kD + 2) * sizeof(float) + 32;
 }
-size_t pool_bytes(int Hkv, long long num_pages, int page_size, int d) {
-    return ((size_t)num_pages * Hkv * page_size * d * 2 + 255) & ~size_t(255);
+size_t up(size_t n, size_t to) { return (n + to - 1) & ~(to - 1); }
+// bytes of a pool of `pages` bf16 pages
+size_t pool_bytes(const PagedCache& c, long long pages) {
+    return up((size_t)pages * c.Hkv * c.page_size * c.d * 2, 256);
+}
+// The bf16 copy of 8-bit pages: with room for every page of the cache, by its
+// number, or for the block table's entries, by theirs, with a table, where that
+// halves it (a call on a few sequences of a large cache). The table is not free:
+// 63 prompts of 216 tokens in a cache of 255 pages took 127 us by page and 131 by
+// entry. max_blocks == 0: not known.
+struct Copy {
+    bool by_entry;
+    size_t table, pool;  // bytes of the table and of each of K and V
+};
+Copy copy_of(const PagedCache& c) {
+    const Copy by_page = {false, 0, pool_bytes(c, c.num_pages)};
+    const long long entries = (long long)c.B * c.max_blocks;
+    if (entries == 0 || 2 * entries > c.num_pages) return by_page;
+    const Copy by_entry = {true, up((size_t)entries * sizeof(int32_t), 256), pool_bytes(c, entries)};
+    return by_entry.table + 2 * by_entry.pool < 2 * by_page.pool ? by_entry : by_page;  // (never more than by page)
 }
 
 }  // namespace
@@ -1093,31 +1114,39 @@ size_t pool_bytes(int Hkv, long long num_pages, int page_size, int d) {
 bool paged_pre_supported(const PagedFwdArgs& a) {
     // (a scale <= 0 goes to the other kernels: the dense softmax step takes a
     // row's maximum before it scales)
+    if (a.k_scale && ((long long)a.c.B * a.c.max_blocks > 0x7fffffffLL || a.c.Hkv > 65535)) return false;  // the copy's grid
     return a.dtype == MODA_BF16 && a.c.d % 8 == 0 && a.G <= 128 && a.c.page_size % 16 == 0 && a.scale > 0.f &&
            (long long)a.c.N * a.Hq < (1LL << 31);
 }
 
-size_t paged_pre_workspace(int Hkv, int d, long long num_pages, int page_size, bool q8) {
-    const size_t parts = (join_bytes() + 255) & ~size_t(255);
-    return q8 ? parts + 2 * pool_bytes(Hkv, num_pages, page_size, d) + 32 : parts;
+size_t paged_pre_workspace(const PagedCache& c, bool q8) {
+    const size_t parts = up(join_bytes(), 256);
+    if (!q8) return parts;
+    const Copy copy = copy_of(c);
+    return parts + copy.table + 2 * copy.pool + 32;
 }
 
 cudaError_t launch_paged_pre(const PagedFwdArgs& a, cudaStream_t s) {
     char* ws = static_cast<char*>(a.workspace);
     if (!a.k_scale) return launch(a, ws, s);
-    // [parts | bf16 K pages | bf16 V pages], the pages at 32-byte boundaries
+    // [parts | table | bf16 K pages | bf16 V pages], the pages at 32-byte boundaries
     const PagedCache& c = a.c;
-    char* pages = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws + ((join_bytes() + 255) & ~size_t(255))) + 31) & ~uintptr_t(31));
-    const size_t pool = pool_bytes(c.Hkv, c.num_pages, c.page_size, c.d);
+    const Copy copy = copy_of(c);
+    char* at = reinterpret_cast<char*>(up(reinterpret_cast<uintptr_t>(ws + up(join_bytes(), 256)), 32));
+    int32_t* table = copy.by_entry ? reinterpret_cast<int32_t*>(at) : nullptr;
+    at += copy.table;
     PagedFwdArgs f = a;
-    f.k_pages = pages;
-    f.v_pages = pages + pool;
+    f.k_pages = at;
+    f.v_pages = at + copy.pool;
     f.k_scale = f.v_scale = nullptr;
     const long long blocks = (long long)c.B * c.max_blocks;
-    if (blocks > 0x7fffffffLL || c.Hkv > 65535) return cudaErrorInvalidValue;
+    if (copy.by_entry) {
+        f.c.block_table = table;
+        f.c.num_pages = (int)blocks;
+    }
     paged_dequant_kernel<<<dim3((unsigned)std::min(blocks, 4096LL), c.Hkv), 256, 0, s>>>(
         c, static_cast<const int8_t*>(a.k_pages), static_cast<const int8_t*>(a.v_pages), a.k_scale, a.v_scale,
-        reinterpret_cast<__nv_bfloat16*>(pages), reinterpret_cast<__nv_bfloat16*>(pages + pool));
+        reinterpret_cast<__nv_bfloat16*>(at), reinterpret_cast<__nv_bfloat16*>(at + copy.pool), table);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? launch(f, ws, s) : e;
 }

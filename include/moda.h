@@ -444,15 +444,26 @@ moda_status moda_paged_append_q8(const void* q, const void* k, const void* v,
  *                  chunks over 8-bit pages (max_q * Hq / Hkv of 33 and more;
  *                  q8 != 0 in the size's call) it also holds the pages in
  *                  use as bf16, in two pools of num_pages pages; one
- *                  workspace serves all layers.
+ *                  workspace serves all layers. moda_fwd_paged_q8_ex needs less.
  * The attention does not append: call moda_paged_append first, with the same
  * cu_q, ctx_lens and block_table. moda_fwd_paged_q8 reads 8-bit pages; depth
  * rows stay in `dtype`. bf16 with d % 8 == 0 (8-bit pages: d % 16 == 0) and
  * page_size % 16 == 0 runs on the tensor cores, everything else on the SIMT kernels (MODA_IMPL_TC2 is not
  * offered: MODA_ERR_UNSUPPORTED). Errors otherwise as moda_fwd_ex.
+ *
+ * moda_fwd_paged_q8_ex — moda_fwd_paged_q8 with a workspace that goes by the
+ * call and not by the cache: moda_fwd_paged_workspace_bytes_ex knows the block
+ * table's width and the kernel choice, and its bf16 pools have room for
+ * B * max_blocks pages where that is at most half of num_pages. With less than
+ * that size, but at least the one for q8 == 0, a chunk runs too, without the
+ * copy, on the kernel for few rows, which is slower there (two chunks of 1024
+ * tokens over 16K: 3.3 ms against 0.42); below that MODA_ERR_WORKSPACE.
  */
 size_t moda_fwd_paged_workspace_bytes(int N, int B, int max_q, int Hq, int Hkv, int d,
                                       int num_pages, int page_size, moda_dtype dtype, int q8);
+size_t moda_fwd_paged_workspace_bytes_ex(int N, int B, int max_q, int Hq, int Hkv, int d,
+                                         int num_pages, int page_size, int max_blocks,
+                                         moda_dtype dtype, int q8, moda_impl impl);
 moda_status moda_fwd_paged(const void* q, const void* k_pages, const void* v_pages,
                            const void* kd, const void* vd,
                            const int32_t* cu_q, const int32_t* ctx_lens, const int32_t* block_table,
@@ -468,6 +479,15 @@ moda_status moda_fwd_paged_q8(const void* q, const int8_t* k_pages, const int8_t
                               int num_pages, int page_size, int max_blocks, moda_dtype dtype, float scale,
                               void* out, float* lse, void* workspace, size_t workspace_bytes,
                               void* stream, moda_impl impl);
+
+moda_status moda_fwd_paged_q8_ex(const void* q, const int8_t* k_pages, const int8_t* v_pages,
+                                 const float* k_scale, const float* v_scale,
+                                 const void* kd, const void* vd,
+                                 const int32_t* cu_q, const int32_t* ctx_lens, const int32_t* block_table,
+                                 int N, int B, int max_q, int Hq, int Hkv, int d, int Ld, int Ld_cap,
+                                 int num_pages, int page_size, int max_blocks, moda_dtype dtype, float scale,
+                                 void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                 void* stream, moda_impl impl);
 
 /* moda_fwd reading depth keys/values from moda_pack_depth's layout. */
 moda_status moda_fwd_packed(const void* q, const void* k, const void* v,

@@ -31,12 +31,12 @@ def cuda(x):
     return {n: t.cuda() if torch.is_tensor(t) else t for n, t in x.items()}
 
 
-def check(got, x, c, scale=None):
+def check(got, x, c, scale=None, keys=302):
     torch.cuda.synchronize()
     assert moda.moda_device_status() == 0
     w = oracle.paged_forward(x["q"], x["k_pages"], x["v_pages"], x["table"], x["cu_q"], x["ctx"], x["kd"], x["vd"], c.Ld,
                              scale or c.d ** -0.5, x["k_scale"], x["v_scale"])
-    check_rows(*got, w, c.dtype, 800, c.d)
+    check_rows(*got, w, c.dtype, keys, c.d)
 
 
 @pytest.mark.gpu
@@ -49,3 +49,98 @@ def test_no_more_than_the_kernel_that_runs_needs(kw):
     few = moda.moda_fwd_paged_workspace_bytes(c.N, 2, 4, 8, 1, c.d, x["k_pages"].shape[0], c.P, torch.bfloat16, True)
     ws = torch.empty(few, dtype=torch.uint8, device="cuda")
     check(run(cuda(x), c, workspace=ws, **kw), x, c, kw.get("scale"))
+
+
+def test_goes_by_the_call_where_the_width_is_known():
+    """Chunks over 8-bit pages: room for the table's entries, not for the pool."""
+    parts = size(q8=False)
+    page = 2 * 16 * 128 * 2                                   # bytes of a bf16 page of 2 heads
+    for pages in (1000, 100000):
+        n = size(pages=pages, max_blocks=6)
+        assert parts + 2 * 12 * page <= n <= parts + 2 * 12 * page + 2048
+        assert size(pages=pages) >= parts + 2 * pages * page
+    assert size(pages=1000, max_blocks=900) == size(pages=1000)   # never more than for the pool
+    assert size(max_blocks=6, q8=False) == parts
+    assert size(max_blocks=6, max_q=1) == size(max_q=1)
+    assert size(max_blocks=6, impl="simt") == 0
+    assert size(max_blocks=0) == 0
+    for pages in range(8, 40):
+        for blocks in range(1, 25):
+            n = size(pages=pages, max_blocks=blocks, Hkv=1)
+            assert n <= size(pages=pages, Hkv=1)
+
+
+# two sequences in a cache of many pages
+LARGE = Paged("large", ((300, 70), (95, 40)), Hq=8, Hkv=2, Ld=2, cap=2)
+
+
+def in_a_large_cache(c, pages):
+    """The call's pages scattered over a pool of `pages`; scales elsewhere NaN."""
+    x = make(c, q8=True)
+    n = x["k_pages"].shape[0]
+    at = torch.arange(n) * (pages // n) + 3
+    g = cuda(x)
+    for name in ("k_pages", "v_pages", "k_scale", "v_scale"):
+        fill = float("nan") if name.endswith("scale") else 77
+        pool = torch.full((pages, *x[name].shape[1:]), fill, dtype=x[name].dtype, device="cuda")
+        pool[at] = g[name]
+        g[name] = pool
+    g["table"] = torch.where(x["table"] < 0, x["table"], at[x["table"].clamp(min=0)].to(torch.int32)).cuda()
+    return x, g
+
+
+@pytest.mark.gpu
+def test_a_chunk_in_a_large_cache_takes_little():
+    c = LARGE
+    x, g = in_a_large_cache(c, 20000)
+    pool = g["k_pages"].numel() * 2 * 2                      # bytes of both bf16 pools
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    got = run(g, c)
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() - before < pool / 4
+    check(got, x, c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pages", [40, 20000], ids=["small_pool", "large_pool"])
+@pytest.mark.parametrize("copy", [True, False], ids=["with_copy", "without_copy"])
+@pytest.mark.parametrize("shift", [0, 16])
+def test_exactly_the_bytes_asked_for(pages, copy, shift):
+    """A workspace of the size asked for, or of the size for 16-bit pages: right
+    rows, and nothing behind or before it is written."""
+    c = LARGE
+    x, g = in_a_large_cache(c, pages)
+    n = moda.moda_fwd_paged_workspace_bytes(c.N, 2, x["max_q"], c.Hq, c.Hkv, c.d, pages, c.P, torch.bfloat16, copy,
+                                            max_blocks=x["table"].shape[1])
+    whole = torch.full((256 + n + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+    ws = whole[256 + shift:256 + shift + n]
+    check(run(g, c, workspace=ws), x, c)
+    assert torch.all(whole[:256 + shift] == 0xAB) and torch.all(whole[256 + shift + n:] == 0xAB)
+    with pytest.raises(moda.ModaError):
+        few = moda.moda_fwd_paged_workspace_bytes(c.N, 2, 8, c.Hq, c.Hkv, c.d, pages, c.P, torch.bfloat16, False)
+        run(g, c, workspace=whole[:few - 256])
+
+
+@pytest.mark.gpu
+def test_a_chunk_runs_where_the_copy_does_not_fit():
+    c = Paged("full", ((9000, 70), (8700, 40)), Hq=8, Hkv=8, Ld=2, cap=2)
+    x = make(c, q8=True)
+    g = cuda(x)
+    n = moda.moda_fwd_paged_workspace_bytes(c.N, 2, x["max_q"], c.Hq, c.Hkv, c.d, x["k_pages"].shape[0], c.P,
+                                            torch.bfloat16, True, max_blocks=x["table"].shape[1])
+    few = moda.moda_fwd_paged_workspace_bytes(c.N, 2, x["max_q"], c.Hq, c.Hkv, c.d, x["k_pages"].shape[0], c.P,
+                                              torch.bfloat16, False)
+    assert n > few + (60 << 20)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    limit = torch.cuda.memory_reserved() + few + (24 << 20)   # room for the parts, not for the copy
+    torch.cuda.set_per_process_memory_fraction(limit / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        got = run(g, c)
+        torch.cuda.synchronize()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    check(got, x, c, keys=9002)
