@@ -73,9 +73,9 @@ bool paged_pre_supported(const PagedFwdArgs& a);
 size_t paged_pre_workspace(const PagedCache& c, bool q8);  // c.max_blocks may be 0: not known
 cudaError_t launch_paged_pre(const PagedFwdArgs& a, cudaStream_t s);
 // Rows per sequence and kv-head from which it is the one that runs. 48
-// sequences of 3000 tokens, 33 to 40 rows: G = 8 78 us against 116 on the other
-// kernel, G = 1 166 against 320, 8-bit pages 290 against 442; at 32 rows 78
-// against 75 and, on 8-bit pages, 143 against 93.
+// sequences of 3000 tokens, 4 kv-heads of 128, in us, this kernel / the other:
+// 32 rows 87 / 81 (8-bit pages 162 / 96), 40 rows 87 / 140 (164 / 169), 64 rows
+// 90 / 144 (165 / 172), 128 rows 95 / 264 (171 / 323); G = 1 and 8 alike.
 constexpr int kPagedPreRows = 33;
 // Every shape (moda_paged_simt.cu).
 cudaError_t launch_paged_fwd_simt(const PagedFwdArgs& a, cudaStream_t s);

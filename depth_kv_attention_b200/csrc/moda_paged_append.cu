@@ -1,5 +1,6 @@
 // Appending to the paged sequence cache: the new tokens' keys (rotated by
-// their position), values and rotated queries, in one launch.
+// their position), values and rotated queries, in one launch (8-bit pages with
+// many queries: two, side by side).
 //
 // What it computes, per token at position p of its sequence and per head:
 //   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin)   over the rot/2 pairs
@@ -512,8 +513,8 @@ __device__ __forceinline__ void page_run(const AppendArgs& a, int i, const Token
 // for one kv-head. Without Q (no queries, or the bulk form takes them) the code
 // for them is not there. Three CTAs per SM even at the price of some spills in
 // the queries' part: with one, a decode step of 64 tokens ran in two waves (10.0
-// us, with three 5.8). 16000 tokens into pages of 32 rows, 4 kv-heads: 23 us, and
-// 33 us for the queries.
+// us, with three 5.8). 8 chunks, 9975 tokens, into pages of 32 rows, 4 kv-heads:
+// 23 us, and 33 us for the queries (163 MB: 4.9 TB/s).
 template <typename T, int VEC, bool INTER, bool Q>
 __global__ void __launch_bounds__(2 * kRunThreads, 3)
 paged_append_q8_kernel(const AppendArgs a, int shares, int q_blocks, int chunk) {
@@ -593,9 +594,11 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
     const int h_first = a.q ? 0 : a.Hq, h_all = q8 ? a.Hq : a.Hq + 2 * c.Hkv;
     const int heads = h_all - h_first;  // of the token warps (8-bit pages: q only)
     const bool bulk = VEC > 1 && (long long)c.N * heads * c.d * (long long)sizeof(T) >= kBulkBytes;
-    if (bulk) {
-        const cudaError_t e = launch_bulk<T, VEC, INTER>(a, h_first, h_all, s);
-        if (e != cudaSuccess || !q8) return e;
+    if constexpr (VEC > 1) {
+        if (bulk) {
+            const cudaError_t e = launch_bulk<T, VEC, INTER>(a, h_first, h_all, s);
+            if (e != cudaSuccess || !q8) return e;
+        }
     }
     // few tokens: split a token's heads until about 16 warps per SM are busy
     int shares = 1;
@@ -615,8 +618,8 @@ cudaError_t launch(const AppendArgs& a, cudaStream_t s) {
         if (q_blocks) {
             paged_append_q8_kernel<T, VEC, INTER, true><<<(unsigned)all, 2 * kRunThreads, 0, s>>>(a, shares, (int)q_blocks, chunk);
         } else {
-            // beside the queries' kernel, where that went ahead (16000 tokens: 56 us one
-            // after the other, 51 side by side; one of 4096 37 and 30)
+            // beside the queries' kernel, where that went ahead (8 chunks, 9975 tokens: 56 us
+            // one after the other, 51 side by side; one of 4096 37 and 30)
             cudaLaunchConfig_t cfg;
             std::memset(&cfg, 0, sizeof(cfg));
             cfg.gridDim = dim3((unsigned)all);

@@ -21,7 +21,9 @@
 //    has (G heads of a token), where a tcgen05 tile would be 128 rows high. Four
 //    consumer warps, each with its own keys of a stage and its own softmax state,
 //    joined at the unit's end; with 32 rows two of them take 16 rows each of the
-//    same keys. Up to 8 rows three CTAs fit an SM, else two. P^T is
+//    same keys. Up to 8 rows three CTAs fit an SM, else two. For d > 64 that
+//    takes some spills: 92 and 180 bytes of stores a thread with 16 and 32 rows,
+//    over 8-bit pages 84, 308 and 308 with 8, 16 and 32. P^T is
 //    what the second product wants as its B operand, once its 8 x 8 blocks are
 //    transposed between lanes (movmatrix).
 //  * 8-bit pages: a lane reads whole 16-byte pieces of a row and turns codes
@@ -365,7 +367,8 @@ __device__ __forceinline__ void clear_keys(uint32_t slice, uint32_t bad, int lan
     }
 }
 
-// Box of 16 rows x 64 bf16 (or 128 codes) into shared memory.
+// Box of 16 rows x 64 bf16 (or 128 codes) to a shared memory address: as
+// ptx::tma_load_4d, whose generic pointer took registers here (28 bytes more of spills).
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, uint64_t* bar, int x, int row, int h, int page) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
@@ -960,14 +963,15 @@ int rows_of(int max_q, int G) {
     return r <= 8 ? 8 : r <= 16 ? 16 : 32;
 }
 
-bool encode(CUtensorMap* m, bool u8, const void* base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
-            const cuuint32_t (&box)[4]) {
+// Map of 8-bit pages with the swizzle of the bf16 ones.
+bool make_tmap_codes(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+                     const cuuint32_t (&box)[4]) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return false;
     const cuuint32_t es[4] = {1, 1, 1, 1};
-    return enc(m, u8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
-               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool Q8, int NH, int NR, int WR>
@@ -981,15 +985,17 @@ cudaError_t launch(const PagedFwdArgs& a, cudaStream_t s) {
         const cuuint64_t dims[4] = {d, P, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_pages};
         const cuuint64_t st[3] = {d * e, P * d * e, c.Hkv * P * d * e};
         const cuuint32_t box[4] = {Q8 ? 128u : 64u, (cuuint32_t)kSliceRows, 1, 1};
-        if (!encode(&p.tm_k, Q8, a.k_pages, dims, st, box) || !encode(&p.tm_v, Q8, a.v_pages, dims, st, box))
-            return cudaErrorInvalidValue;
+        auto make = [&](CUtensorMap* m, const void* pages) {
+            return Q8 ? make_tmap_codes(m, pages, dims, st, box) : make_tmap_bf16_4d(m, pages, dims, st, box);
+        };
+        if (!make(&p.tm_k, a.k_pages) || !make(&p.tm_v, a.v_pages)) return cudaErrorInvalidValue;
     }
     if (a.Ld > 0) {
         // dimensions: feature, kv-head, slot (those in use), token
         const cuuint64_t dims[4] = {d, (cuuint64_t)c.Hkv, (cuuint64_t)a.Ld, (cuuint64_t)c.N};
         const cuuint64_t st[3] = {d * 2, c.Hkv * d * 2, (cuuint64_t)a.Ld_cap * c.Hkv * d * 2};
         const cuuint32_t box[4] = {64, 1, (cuuint32_t)kSliceRows, 1};
-        if (!encode(&p.tm_kd, false, a.kd, dims, st, box) || !encode(&p.tm_vd, false, a.vd, dims, st, box))
+        if (!make_tmap_bf16_4d(&p.tm_kd, a.kd, dims, st, box) || !make_tmap_bf16_4d(&p.tm_vd, a.vd, dims, st, box))
             return cudaErrorInvalidValue;
     } else {
         p.tm_kd = p.tm_k;
@@ -1045,7 +1051,7 @@ cudaError_t by_rows(const PagedFwdArgs& a, cudaStream_t s) {
 
 bool paged_dec_supported(const PagedFwdArgs& a) {
     const PagedCache& c = a.c;
-    if (a.dtype != MODA_BF16 || c.d % 8 || c.d > 128 || c.page_size % kSliceRows) return false;
+    if (a.dtype != MODA_BF16 || c.d % 8 || c.page_size % kSliceRows) return false;
     if (a.k_scale && c.d % 16) return false;  // TMA strides are multiples of 16 bytes
     return (long long)c.N * a.Hq < (1LL << 31);
 }

@@ -1050,7 +1050,6 @@ cudaError_t launch(const PagedFwdArgs& a, char* ws, cudaStream_t s) {
 __global__ void __launch_bounds__(256) paged_dequant_kernel(const PagedCache c, const int8_t* kc, const int8_t* vc,
                                                             const float* ks, const float* vs, __nv_bfloat16* ko,
                                                             __nv_bfloat16* vo, int32_t* table) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int h = blockIdx.y;
     const int total = c.B * c.max_blocks;
     for (int x = blockIdx.x; x < total; x += gridDim.x) {

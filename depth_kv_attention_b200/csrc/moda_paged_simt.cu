@@ -1,6 +1,6 @@
 // Scalar (SIMT, fp32 FMA) attention over the paged sequence cache: the path
 // for fp32 and for the shapes the tensor-core kernels do not take (pages that
-// are no multiple of 16 rows, d no multiple of 8).
+// are no multiple of 16 rows, 8-bit pages with d no multiple of 16).
 //
 // One softmax over the token's visible sequence keys and its own depth keys
 // ("动态混合深度注意力机制MoDA技术解析", mhpn.cn, §1.2 formula; §2.2 online softmax
