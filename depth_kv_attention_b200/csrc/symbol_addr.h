@@ -12,10 +12,11 @@
 // mutex, so concurrent first calls from several host threads are safe.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <mutex>
+
+#include "context_id.h"
 
 namespace moda {
 
@@ -34,7 +35,7 @@ class SymbolAddr {
         if (e != cudaSuccess) return e;
         if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
         unsigned long long id = 0;
-        const bool have_id = context_id(&id);
+        const bool have_id = current_context_id(&id);
         std::lock_guard<std::mutex> lock(mu_);
         Entry& en = table_[dev];
         if (en.addr && have_id && en.ctx_id == id) {
@@ -46,7 +47,7 @@ class SymbolAddr {
         if (e != cudaSuccess) return e;
         // the context exists now even if it did not before the call
         unsigned long long id2 = 0;
-        const bool have_id2 = context_id(&id2);
+        const bool have_id2 = current_context_id(&id2);
         en.addr = a;
         en.ctx_id = have_id2 ? id2 : 0;
         *out = a;
@@ -59,33 +60,6 @@ class SymbolAddr {
         void* addr = nullptr;
         unsigned long long ctx_id = 0;
     };
-
-    typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
-    typedef CUresult (*CtxGetIdFn)(CUcontext, unsigned long long*);
-
-    // Unique id of the calling thread's current context; false when there is
-    // none yet or the driver does not offer the query (then every call
-    // resolves the address again, which is correct, only slower).
-    static bool context_id(unsigned long long* id) {
-        static CtxGetCurrentFn get_current = nullptr;
-        static CtxGetIdFn get_id = nullptr;
-        static std::once_flag once;
-        std::call_once(once, [] {
-            void* f = nullptr;
-            cudaDriverEntryPointQueryResult q;
-            if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &f, cudaEnableDefault, &q) == cudaSuccess &&
-                q == cudaDriverEntryPointSuccess)
-                get_current = reinterpret_cast<CtxGetCurrentFn>(f);
-            f = nullptr;
-            if (cudaGetDriverEntryPoint("cuCtxGetId", &f, cudaEnableDefault, &q) == cudaSuccess &&
-                q == cudaDriverEntryPointSuccess)
-                get_id = reinterpret_cast<CtxGetIdFn>(f);
-        });
-        if (!get_current || !get_id) return false;
-        CUcontext ctx = nullptr;
-        if (get_current(&ctx) != CUDA_SUCCESS || !ctx) return false;
-        return get_id(ctx, id) == CUDA_SUCCESS;
-    }
 
     const void* symbol_;
     std::mutex mu_;
