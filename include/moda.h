@@ -434,6 +434,8 @@ moda_status moda_paged_append_q8(const void* q, const void* k, const void* v,
  *   softmax's denominator. A row that sees nothing (Ld = 0 and no position or
  *   no page) gets zeros and lse = -inf. Keys a row does not see never reach
  *   it, whatever they hold (NaN and infinities included).
+ *   The sums over keys are held in fp32 before they are divided by the sum of
+ *   P, whose largest may be up to 2^8: values of 2^100 and more may overflow.
  *   q, out [N,Hq,d]; lse [N,Hq] fp32 (may be NULL); kd, vd [N,Ld_cap,Hkv,d]
  *   with Ld <= Ld_cap slots in use (NULL iff Ld == 0).
  *   max_q      in  about the most new tokens any sequence has; it only selects
