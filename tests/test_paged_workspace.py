@@ -144,3 +144,25 @@ def test_a_chunk_runs_where_the_copy_does_not_fit():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     check(got, x, c, keys=9002)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(ks=None), 1), (dict(vs=None), 1), (dict(q=None), 1), (dict(max_q=0), 1), (dict(scale=float("nan")), 1),
+    (dict(impl=3), 2), (dict(d=20), 2), (dict(kp=0x10008), 3), (dict(ws=0x10008), 3),
+    (dict(ws=None), 4), (dict(nbytes=-1), 4), (dict(nbytes=0), 4),
+])
+def test_refusals_of_the_c_entry(change, code):
+    """Decided before any CUDA call (fake addresses, never dereferenced).
+    nbytes -1: one less than the kernel for few rows needs."""
+    import ctypes
+    A = 0x10000
+    vp, i = ctypes.c_void_p, ctypes.c_int
+    x = dict(q=A, kp=A, vp=A, ks=A, vs=A, max_q=90, d=128, scale=0.1, ws=A, nbytes=1 << 40, impl=0)
+    x.update(change)
+    if x["nbytes"] == -1:
+        x["nbytes"] = moda.moda_fwd_paged_workspace_bytes(99, 2, 8, 8, 2, 128, 1000, 16, torch.bfloat16, False) - 1
+    fn = moda.lib.moda_fwd_paged_q8_ex
+    fn.restype = i
+    fn.argtypes = [vp] * 10 + [i] * 12 + [ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp, i]
+    assert fn(x["q"], x["kp"], x["vp"], x["ks"], x["vs"], None, None, A, A, A, 99, 2, x["max_q"], 8, 2, x["d"], 0, 0, 1000,
+              16, 3, 0, x["scale"], A, A, x["ws"], x["nbytes"], None, x["impl"]) == code
