@@ -1,4 +1,8 @@
 """The workspace that the paged attention asks for, and what it does with one."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -7,6 +11,9 @@ from paged_util import Paged, check_rows, make
 
 moda = pytest.importorskip("depth_kv_attention_b200",
                            reason="libmoda.so not built (python depth_kv_attention_b200/csrc/build.py)")
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def size(max_q=90, Hq=8, Hkv=2, d=128, pages=1000, page=16, dtype=torch.bfloat16, q8=True, **kw):
@@ -124,8 +131,7 @@ def test_exactly_the_bytes_asked_for(pages, copy, shift):
         run(g, c, workspace=whole[:few - 256])
 
 
-@pytest.mark.gpu
-def test_a_chunk_runs_where_the_copy_does_not_fit():
+def copy_does_not_fit():
     c = Paged("full", ((9000, 70), (8700, 40)), Hq=8, Hkv=8, Ld=2, cap=2)
     x = make(c, q8=True)
     g = cuda(x)
@@ -136,14 +142,22 @@ def test_a_chunk_runs_where_the_copy_does_not_fit():
     assert n > few + (60 << 20)
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
     limit = torch.cuda.memory_reserved() + few + (24 << 20)   # room for the parts, not for the copy
     torch.cuda.set_per_process_memory_fraction(limit / torch.cuda.get_device_properties(0).total_memory)
-    try:
-        got = run(g, c)
-        torch.cuda.synchronize()
-    finally:
-        torch.cuda.set_per_process_memory_fraction(1.0)
+    got = run(g, c)
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() - before < few + (24 << 20)
+    torch.cuda.set_per_process_memory_fraction(1.0)
     check(got, x, c, keys=9002)
+
+
+@pytest.mark.gpu
+def test_a_chunk_runs_where_the_copy_does_not_fit():
+    """In a process of its own, whose allocator holds nothing that would serve it."""
+    code = "import sys; sys.path[:0] = ['.', 'tests']; import test_paged_workspace as t; t.copy_does_not_fit()"
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-3000:]
 
 
 @pytest.mark.parametrize("change,code", [
