@@ -394,9 +394,10 @@ def _binding():
         except ImportError as e:
             raise ImportError(f"depth_kv_attention_b200/_moda_torch.so does not load ({e}): build it with "
                               "`python depth_kv_attention_b200/csrc/build.py`") from e
-        if _moda_torch.torch_version != torch.__version__:
-            raise ImportError(f"depth_kv_attention_b200/_moda_torch.so is of torch {_moda_torch.torch_version}, not "
-                              f"{torch.__version__}: build it again with `python depth_kv_attention_b200/csrc/build.py`")
+        built_for = getattr(_moda_torch, "torch_version", "unknown")
+        if built_for != torch.__version__:
+            raise ImportError(f"depth_kv_attention_b200/_moda_torch.so is of torch {built_for}, not {torch.__version__}: "
+                              "build it again with `python depth_kv_attention_b200/csrc/build.py`")
         _bind = _moda_torch
     return _bind
 

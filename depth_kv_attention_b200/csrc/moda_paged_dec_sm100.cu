@@ -31,7 +31,7 @@
 //    order in which a lane holds features is free in a product's contracted
 //    index (queries are laid out alike) and only permutes the output rows.
 //    A key's scale multiplies its logit, a value's scale its codes or its P
-//    (value_scale): all exact, as scales are powers of two.
+//    (code_factor, p_factor): all exact, as scales are powers of two.
 //  * Rounding: logits, P, l, O in fp32; P is rounded to bf16 as the operand of
 //    P V (l sums the unrounded P).
 //  * A value that a row must not see may be anything: a masked P is exactly 0,

@@ -100,6 +100,21 @@ def test_binding_of_another_torch_is_refused(monkeypatch):
         moda.moda_fwd_paged(z, z, z, z, z, z, 1)
 
 
+def test_a_binding_that_does_not_say_its_torch_is_refused(monkeypatch):
+    import types
+
+    import torch
+
+    import depth_kv_attention_b200 as moda
+    old = types.ModuleType("_moda_torch")
+    monkeypatch.setattr(moda, "_bind", None)
+    monkeypatch.setitem(sys.modules, "depth_kv_attention_b200._moda_torch", old)
+    monkeypatch.setattr(moda, "_moda_torch", old, raising=False)
+    z = torch.zeros(1)
+    with pytest.raises(ImportError, match="build it again"):
+        moda.moda_fwd_paged(z, z, z, z, z, z, 1)
+
+
 def test_a_flag_without_a_truth_value_is_refused():
     """Before anything runs, and not as a result with an error pending."""
     import torch
