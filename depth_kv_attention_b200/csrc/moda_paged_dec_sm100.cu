@@ -1053,7 +1053,7 @@ bool paged_dec_supported(const PagedFwdArgs& a) {
     const PagedCache& c = a.c;
     if (a.dtype != MODA_BF16 || c.d % 8 || c.page_size % kSliceRows) return false;
     if (a.k_scale && c.d % 16) return false;  // TMA strides are multiples of 16 bytes
-    return (long long)c.N * a.Hq < (1LL << 31);
+    return (long long)c.N * a.Hq < 0x7fffff00LL;  // rows in 32 bits, the last tile's end among them
 }
 
 size_t paged_dec_workspace(int max_q, int G, int d) {

@@ -1113,9 +1113,10 @@ Copy copy_of(const PagedCache& c) {
 bool paged_pre_supported(const PagedFwdArgs& a) {
     // (a scale <= 0 goes to the other kernels: the dense softmax step takes a
     // row's maximum before it scales)
-    if (a.k_scale && ((long long)a.c.B * a.c.max_blocks > 0x7fffffffLL || a.c.Hkv > 65535)) return false;  // the copy's grid
+    // (the copy's grid, and its index, which runs past the entries by up to a grid)
+    if (a.k_scale && ((long long)a.c.B * a.c.max_blocks > 0x7fff0000LL || a.c.Hkv > 65535)) return false;
     return a.dtype == MODA_BF16 && a.c.d % 8 == 0 && a.G <= 128 && a.c.page_size % 16 == 0 && a.scale > 0.f &&
-           (long long)a.c.N * a.Hq < (1LL << 31);
+           (long long)a.c.N * a.Hq < 0x7fffff00LL;  // rows in 32 bits, the last tile's end among them
 }
 
 size_t paged_pre_workspace(const PagedCache& c, bool q8) {

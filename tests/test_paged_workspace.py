@@ -180,3 +180,16 @@ def test_refusals_of_the_c_entry(change, code):
     fn.argtypes = [vp] * 10 + [i] * 12 + [ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp, i]
     assert fn(x["q"], x["kp"], x["vp"], x["ks"], x["vs"], None, None, A, A, A, 99, 2, x["max_q"], 8, 2, x["d"], 0, 0, 1000,
               16, 3, 0, x["scale"], A, A, x["ws"], x["nbytes"], None, x["impl"]) == code
+
+
+def test_sizes_whose_indexes_would_pass_32_bits_take_another_kernel():
+    """The last row tile's end, and the conversion's index over the table's
+    entries behind the last one, have to fit 32 bits too."""
+    def n(N, Hq=1, B=2, max_blocks=6, q8=False, max_q=90, d=8):
+        return moda.moda_fwd_paged_workspace_bytes(N, B, max_q, Hq, 1, d, 1 << 30, 16, torch.bfloat16, q8,
+                                                   max_blocks=max_blocks)
+    assert n(0x7fffff00 - 1) > 0
+    assert n(0x7fffff00) == 0 and n(0x7fffffff) == 0          # the scalar path, which needs none
+    few = n(99, max_q=32, d=16)
+    assert n(99, B=1, max_blocks=0x7fff0000, q8=True, d=16) > few   # the copy of the pages
+    assert n(99, B=1, max_blocks=0x7fff0001, q8=True, d=16) == few  # the kernel for few rows
